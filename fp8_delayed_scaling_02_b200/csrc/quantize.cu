@@ -34,8 +34,11 @@
 #include <algorithm>
 #include <cstring>
 
+#include "amax_fold.cuh"
 #include "common.cuh"
+#include "elem_io.cuh"
 #include "fp8_ring.cuh"
+#include "host_util.cuh"
 
 namespace fp8ds {
 namespace {
@@ -43,126 +46,6 @@ namespace {
 constexpr int kThreads = 256;     // tile, amax and fallback kernels
 constexpr int kRowThreads = 256;  // ROW kernel block size
 constexpr int kRowMinChunks = 2;  // 16-element chunks per ROW thread, at least
-
-// Three modes: fold (history set, amax_out null), local (amax_out set: the
-// last block writes the grid's amax and scale_inv and does not fold; the
-// fold follows after a cross-rank MAX of the amax) and fixed scale (both
-// null: current scaling's cast pass).
-struct RingArgs {
-  float* history;
-  int32_t* idx;
-  float* scale;
-  float* scale_inv;
-  uint32_t* scratch;
-  float* amax_out;
-};
-
-// ---- element loads -----------------------------------------------------------
-
-template <int DT> struct In;
-template <> struct In<FP8_IN_BF16> { static constexpr int kBytes = 2; };
-template <> struct In<FP8_IN_FP16> { static constexpr int kBytes = 2; };
-template <> struct In<FP8_IN_FP32> { static constexpr int kBytes = 4; };
-
-template <int DT>
-__device__ __forceinline__ float load_one(const uint8_t* p) {
-  if constexpr (DT == FP8_IN_BF16) {
-    return __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(p)) << 16);
-  } else if constexpr (DT == FP8_IN_FP16) {
-    return __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(p)));
-  } else {
-    return *reinterpret_cast<const float*>(p);
-  }
-}
-
-// Two 16-bit elements packed in one word -> floats (low half first).
-template <int DT>
-__device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
-  if constexpr (DT == FP8_IN_BF16) {
-    lo = __uint_as_float(w << 16);
-    hi = __uint_as_float(w & 0xFFFF0000u);
-  } else {
-    __half2 h = *reinterpret_cast<__half2*>(&w);
-    float2 f = __half22float2(h);
-    lo = f.x;
-    hi = f.y;
-  }
-}
-
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
-  return __ldg(reinterpret_cast<const uint4*>(p));
-}
-
-// Words [0, NW) of the byte stream that starts `ph` bytes past the 16-byte
-// aligned address `q`, given the aligned words W[0, NW + 4).  ph is a multiple
-// of the element size; the word shift is selected without dynamic register
-// indexing and the half-word remainder (16-bit types only) is a funnel shift.
-template <int NW>
-__device__ __forceinline__ void realign(const uint32_t (&W)[NW + 4], int ph, uint32_t (&D)[NW]) {
-  const int ws = ph >> 2;
-  uint32_t X[NW + 1];
-#pragma unroll
-  for (int i = 0; i <= NW; ++i) {
-    uint32_t a = W[i], b = W[i + 1], c = W[i + 2], d = W[i + 3];
-    X[i] = ws == 0 ? a : (ws == 1 ? b : (ws == 2 ? c : d));
-  }
-  const bool half = (ph & 2) != 0;
-#pragma unroll
-  for (int i = 0; i < NW; ++i) D[i] = half ? __funnelshift_r(X[i], X[i + 1], 16) : X[i];
-}
-
-// Load N (8 or 16) consecutive elements starting at element address p into v.
-// Only 16-byte granules that hold at least one of the N elements are read.
-template <int DT, int N>
-__device__ __forceinline__ void load_vec(const uint8_t* p, float (&v)[N]) {
-  constexpr int kB = In<DT>::kBytes;
-  constexpr int NW = N * kB / 4;      // useful words
-  constexpr int NG = NW / 4;          // useful granules when aligned
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  const int ph = int(a & 15);
-  const uint8_t* q = p - ph;
-  uint32_t W[NW + 4];
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    uint4 t = ldg16(q + 16 * g);
-    W[4 * g] = t.x; W[4 * g + 1] = t.y; W[4 * g + 2] = t.z; W[4 * g + 3] = t.w;
-  }
-  if (ph != 0) {
-    uint4 t = ldg16(q + 16 * NG);
-    W[4 * NG] = t.x; W[4 * NG + 1] = t.y; W[4 * NG + 2] = t.z; W[4 * NG + 3] = t.w;
-  } else {
-    W[4 * NG] = W[4 * NG + 1] = W[4 * NG + 2] = W[4 * NG + 3] = 0u;
-  }
-  uint32_t D[NW];
-  realign<NW>(W, ph, D);
-  if constexpr (kB == 2) {
-#pragma unroll
-    for (int i = 0; i < NW; ++i) unpack2<DT>(D[i], v[2 * i], v[2 * i + 1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NW; ++i) v[i] = __uint_as_float(D[i]);
-  }
-}
-
-// Aligned fast path (p is 16-byte aligned).
-template <int DT, int N>
-__device__ __forceinline__ void load_vec_aligned(const uint8_t* p, float (&v)[N]) {
-  constexpr int kB = In<DT>::kBytes;
-  constexpr int NW = N * kB / 4;
-#pragma unroll
-  for (int g = 0; g < NW / 4; ++g) {
-    uint4 t = ldg16(p + 16 * g);
-    uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (kB == 2) {
-        unpack2<DT>(w[i], v[8 * g + 2 * i], v[8 * g + 2 * i + 1]);
-      } else {
-        v[4 * g + i] = __uint_as_float(w[i]);
-      }
-    }
-  }
-}
 
 // ---- conversion ------------------------------------------------------------
 
@@ -198,104 +81,6 @@ __device__ __forceinline__ void transpose4x4(uint32_t r0, uint32_t r1, uint32_t 
   c1 = __byte_perm(t0, t2, 0x7632);
   c2 = __byte_perm(t1, t3, 0x5410);
   c3 = __byte_perm(t1, t3, 0x7632);
-}
-
-// ---- amax + ring fold --------------------------------------------------------
-
-// Block-reduce the per-thread amax, publish it with one atomicMax, draw a
-// ticket; the last of the `nblocks` blocks working on this ring folds it.
-// Must be called by every thread of the block.
-// The ring's history and idx are not written until the last block runs, so
-// each block reads them early (prefetch_ring at kernel start, one lane per
-// word) and the fold itself needs no dependent global reads besides the
-// amax word.
-struct RingCache {
-  float hist;  // history[threadIdx.x] for threads 0..15
-  int idx;     // read by thread 16
-};
-
-__device__ __forceinline__ RingCache prefetch_ring(const RingArgs& ring) {
-  RingCache c{0.0f, 0};
-  if (ring.history == nullptr || ring.amax_out != nullptr) return c;  // no fold in this call
-  if (threadIdx.x < kHistoryLen) c.hist = ring.history[threadIdx.x];
-  if (threadIdx.x == kHistoryLen) c.idx = *ring.idx;
-  return c;
-}
-
-// Adds a block's amax m (>= 0) to the ring's amax word and draws the block's
-// ticket (its arrival number among the blocks on this ring).  No fence: the
-// max is an atom that returns only once the word holds the block's amax, and
-// the ticket's address is computed from that return (bit 31 of a
-// non-negative float's bits: 0 at run time, opaque to the compiler), so the
-// ticket cannot be issued before the amax update is performed in L2.  The
-// block that draws the last ticket exchanges the amax word only after that
-// ticket returned -- after every other block's ticket, hence after every
-// other block's amax update, was performed at the same L2 location.  Every
-// global atomic a block issued earlier (the TMA producer's tile claims) must
-// have returned before the block's final barrier for the same reason.  A
-// release-ordered ticket would wait for the block's own output stores to
-// complete; without it a 12.6M-element bf16 row quantize takes 8.6 instead of
-// 9.0 us on B200.
-__device__ __forceinline__ unsigned publish_amax_take_ticket(uint32_t* scratch, float m) {
-  uint32_t old, dep, t;
-  asm volatile("atom.relaxed.gpu.global.max.u32 %0, [%1], %2;" : "=r"(old) : "l"(scratch), "r"(__float_as_uint(m))
-               : "memory");
-  asm volatile("shr.u32 %0, %1, 31;" : "=r"(dep) : "r"(old));
-  asm volatile("atom.relaxed.gpu.global.add.u32 %0, [%1], 1;" : "=r"(t) : "l"(scratch + 1 + dep) : "memory");
-  return t;
-}
-
-template <int FMT, int NT = kThreads>
-__device__ __forceinline__ void amax_ticket_fold(float amax, const RingArgs& ring, float s_used,
-                                                 const RingCache& rc, const unsigned nblocks) {
-  __shared__ float warp_max[NT / 32];
-  __shared__ float hist_s[kHistoryLen];
-  __shared__ int idx_s;
-  __shared__ int last;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-  if (lane == 0) warp_max[warp] = amax;
-  if (threadIdx.x < kHistoryLen) hist_s[threadIdx.x] = rc.hist;
-  if (threadIdx.x == kHistoryLen) idx_s = rc.idx;
-  __syncthreads();
-  if (ring.history == nullptr && ring.amax_out == nullptr) {
-    // Fixed scale: no amax to publish; the last block clears the scratch
-    // words (the tile counter is shared by every kernel that claims tiles).
-    if (threadIdx.x == 0) {
-      unsigned t;
-      asm volatile("atom.relaxed.gpu.global.add.u32 %0, [%1], 1;" : "=r"(t) : "l"(ring.scratch + 1) : "memory");
-      if (t == nblocks - 1) {
-        asm volatile("st.relaxed.gpu.global.u32 [%0], 0;" ::"l"(ring.scratch + 1) : "memory");
-        asm volatile("st.relaxed.gpu.global.u32 [%0], 0;" ::"l"(ring.scratch + 2) : "memory");
-      }
-    }
-    return;
-  }
-  if (threadIdx.x == 0) {
-    float m = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) m = fmaxf(m, warp_max[w]);
-    // (A single 64-bit compare-and-swap carrying amax and ticket was tried:
-    // hundreds of blocks finishing together made its retries quadratic.)
-    const unsigned t = publish_amax_take_ticket(ring.scratch, m);
-    last = (t == nblocks - 1);
-    if (last) {
-      uint32_t bits;
-      asm volatile("atom.relaxed.gpu.global.exch.b32 %0, [%1], 0;" : "=r"(bits) : "l"(ring.scratch) : "memory");
-      const float a = __uint_as_float(bits);
-      asm volatile("st.relaxed.gpu.global.u32 [%0], 0;" ::"l"(ring.scratch + 1) : "memory");
-      asm volatile("st.relaxed.gpu.global.u32 [%0], 0;" ::"l"(ring.scratch + 2) : "memory");  // tile counter
-      if (ring.amax_out != nullptr) {
-        // Local mode: this rank's amax for the cross-rank MAX; the scale the
-        // call used is already known, so its inverse is published now.
-        *ring.amax_out = a;
-        *ring.scale_inv = __frcp_rn(s_used);
-        return;
-      }
-      ring_commit<FMT>(a, hist_s, idx_s, ring.history, ring.idx, ring.scale, ring.scale_inv, s_used);
-    }
-  }
 }
 
 // ---- ROW layout --------------------------------------------------------------
@@ -641,31 +426,6 @@ __device__ __forceinline__ void issue_tile_load_shift(const CUtensorMap* tm, uin
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(r0), "r"(bar)
       : "memory");
-}
-
-// Eight bytes (lo, hi) to an address of any alignment with the widest
-// aligned stores it allows.
-__device__ __forceinline__ void store8_any(uint8_t* o, uint32_t lo, uint32_t hi) {
-  const int m = int(reinterpret_cast<uintptr_t>(o) & 7);
-  if (m == 0) {
-    *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
-  } else if (m == 4) {
-    reinterpret_cast<uint32_t*>(o)[0] = lo;
-    reinterpret_cast<uint32_t*>(o)[1] = hi;
-  } else if ((m & 1) == 0) {
-    uint16_t* h = reinterpret_cast<uint16_t*>(o);
-    h[0] = uint16_t(lo);
-    h[1] = uint16_t(lo >> 16);
-    h[2] = uint16_t(hi);
-    h[3] = uint16_t(hi >> 16);
-  } else {
-    o[0] = uint8_t(lo);
-    uint16_t* h = reinterpret_cast<uint16_t*>(o + 1);
-    h[0] = uint16_t(__byte_perm(lo, 0, 0x0021));
-    h[1] = uint16_t(__byte_perm(lo, hi, 0x0043));
-    h[2] = uint16_t(__byte_perm(hi, 0, 0x0021));
-    o[7] = uint8_t(hi >> 24);
-  }
 }
 
 // Byte offset of 16-byte unit v of transpose-buffer row c (rows of 128 bytes;
@@ -1060,33 +820,6 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(const AmaxArgs a) {
 }
 
 // ---- host side ---------------------------------------------------------------
-
-int sm_count_current() {
-  static int cached[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  if (dev < 0 || dev >= 64) return -1;
-  if (cached[dev] == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-    cached[dev] = n;
-  }
-  return cached[dev];
-}
-
-// Resident blocks per SM of a kernel without dynamic shared memory (cached
-// per device by the caller's static array).
-template <typename Kern>
-int resident_blocks(Kern kern, int threads, int (&cached)[64]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
-  if (cached[dev] == 0) {
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) != cudaSuccess || n < 1) return -1;
-    cached[dev] = n;
-  }
-  return cached[dev];
-}
 
 // ROW grid: one wave of resident blocks at most, and every thread takes the
 // same number of 16-element chunks (at least kRowMinChunks), so no fraction
