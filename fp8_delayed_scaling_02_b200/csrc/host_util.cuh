@@ -2,6 +2,8 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
 
 namespace fp8ds {
 
@@ -30,6 +32,32 @@ int resident_blocks(Kern kern, int threads, int (&cached)[64]) {
     cached[dev] = n;
   }
   return cached[dev];
+}
+
+// Whether p lies on a multiple of `a` bytes (a null pointer does).
+inline bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// An argument's memory.  `over`: an output that may be exactly the memory of
+// an input marked `under` (each element is read before its place is written,
+// by the same thread); every other overlap with an output is a mistake.
+struct Span {
+  const void* p;
+  size_t n;
+  bool out, over, under;
+};
+
+inline bool spans_clash(const Span* s, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (!s[i].out || s[i].p == nullptr || s[i].n == 0) continue;
+    for (int j = 0; j < n; ++j) {
+      if (j == i || s[j].p == nullptr || s[j].n == 0) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p), b = reinterpret_cast<uintptr_t>(s[j].p);
+      if (a >= b + s[j].n || b >= a + s[i].n) continue;
+      if (s[i].over && s[j].under && a == b && s[i].n == s[j].n) continue;
+      return true;
+    }
+  }
+  return false;
 }
 
 }  // namespace fp8ds

@@ -1,4 +1,4 @@
-"""Thin ctypes binding of the fp8ds C ABI (``include/fp8ds.h``).
+"""Thin ctypes binding of the fp8ds C ABI (``include/fp8ds.h``, ``include/fp8ds_layer.h``).
 
 Argument marshalling only: every step of quantize_fp8 and mm_fp8 runs in the
 CUDA kernels of ``libfp8ds.so``.  There is no CPU fallback -- if the library
@@ -7,7 +7,9 @@ device memory and the current stream.
 """
 
 import ctypes
+import functools
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -23,6 +25,8 @@ MM_A_E5M2 = 1 << 8
 MM_B_E5M2 = 1 << 9
 MM_BIAS_E5M2 = 1 << 10
 MM_OUT_BF16, MM_OUT_E4M3, MM_OUT_E5M2 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3
+AUX_ADD, AUX_MUL = 0, 1
 HISTORY_LEN = 16
 
 FP8_OK = 0
@@ -100,6 +104,12 @@ def lib():
         L.fp8_quantize_multi.restype = i32
         L.fp8_mm_ex.argtypes = [vp, vp, ctypes.c_size_t, vp]
         L.fp8_mm_ex.restype = i32
+        L.fp8_rmsnorm.argtypes = [vp, vp]
+        L.fp8_rmsnorm.restype = i32
+        L.fp8_rmsnorm_backward.argtypes = [vp, vp]
+        L.fp8_rmsnorm_backward.restype = i32
+        L.fp8_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
+        L.fp8_rmsnorm_backward_workspace_bytes.restype = ctypes.c_size_t
         L.fp8_launch_count.argtypes = []
         L.fp8_launch_count.restype = ctypes.c_uint64
         _LIB = L
@@ -584,6 +594,179 @@ class Linear:
             _ptr(db), _stream(stream, g.get_device()))
         _check(rc, "fp8_linear_backward")
         return dx, dw, db
+
+
+# ---- the operators around the linear (include/fp8ds_layer.h) -------------------------
+
+
+def _on_stream(fn):
+    """Runs ``fn`` with ``stream`` (default: the current one) and its first tensor's device
+    current, so that what it allocates and launches belongs to that stream."""
+
+    @functools.wraps(fn)
+    def call(x, *args, stream=None, **kw):
+        if not x.is_cuda:
+            raise ValueError("the tensors must be CUDA tensors")
+        if stream is None and x.get_device() == torch.cuda.current_device():
+            return fn(x, *args, **kw)
+        if stream is not None and stream.device != x.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
+        with torch.cuda.device(x.device), torch.cuda.stream(stream):
+            return fn(x, *args, **kw)
+
+    return call
+
+
+def _same(t, like, name, shape=None, dtype=None):
+    """Checks an optional tensor: on ``like``'s device, contiguous, of this shape and type."""
+    if t is None:
+        return
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if tuple(t.shape) != tuple(like.shape if shape is None else shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape if shape is None else shape)}")
+    if t.dtype != (like.dtype if dtype is None else dtype):
+        raise ValueError(f"{name} is {t.dtype}, expected {like.dtype if dtype is None else dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _scalar(t, like, name):
+    if t is not None and (t.device != like.device or t.dtype != torch.float32 or t.numel() != 1):
+        raise ValueError(f"{name} must be a one-element float32 tensor on {like.device}")
+
+
+def _ring_on(ring, like, name):
+    if ring is not None and ring.buf.device != like.device:
+        raise ValueError(f"{name} is on {ring.buf.device}, expected {like.device}")
+
+
+def _gamma_checked(gamma, x):
+    if x.dtype not in IN_DTYPE:
+        raise ValueError(f"{x.dtype} is not one of bfloat16, float16, float32")
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous 2-D tensor")
+    if gamma.dtype != x.dtype and gamma.dtype != torch.float32:
+        raise ValueError(f"gamma is {gamma.dtype}, expected {x.dtype} or float32")
+    _same(gamma, x, "gamma", (x.shape[1],), gamma.dtype)
+    return 1 if gamma.dtype == torch.float32 else 0
+
+
+class CNormArgs(ctypes.Structure):
+    """Mirror of ``fp8_rmsnorm_args``."""
+
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("gamma", ctypes.c_void_p),
+                ("gamma_f32", ctypes.c_int), ("eps", ctypes.c_float), ("h", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("fmt", ctypes.c_int), ("ring", CRing),
+                ("amax_out", ctypes.c_void_p), ("row_sinv", ctypes.c_void_p)]
+
+
+class NormOut(NamedTuple):
+    """What ``rmsnorm`` returns; what was not asked for is None."""
+
+    codes: Optional[torch.Tensor]  # uint8 [rows, cols]
+    sinv: Optional[torch.Tensor]   # ring.scale_inv, or float32 [rows]
+    h: torch.Tensor                # the residual stream (x itself without a residual)
+    rstd: Optional[torch.Tensor]   # float32 [rows]
+    y: Optional[torch.Tensor]      # the norm's output in x's type
+
+
+_NO_RING = CRing()
+
+
+@_on_stream
+def rmsnorm(x, gamma, residual=None, eps=1e-6, fmt=None, ring=None, need_rstd=False, need_y=False, h=None, y=None,
+            codes=None, amax=None):
+    """fp8_rmsnorm: h = x + residual, y = h / rms(h) * gamma, and y's FP8 codes.
+
+    x, residual: contiguous 2-D CUDA tensors (bf16/fp16/fp32); gamma: [cols] of
+    x's type or float32.  fmt E4M3 / E5M2 asks for codes: with ``ring`` (a
+    Ring) on its delayed scale, with the ring folded in the same launch --
+    or, with amax (a one-element float32 CUDA tensor), the amax written there
+    and the fold left to ``ring_fold`` -- and without a ring on one current
+    scale per row.  fmt None returns y alone.  h, y and codes may name the
+    outputs' memory; h or y may be x or residual (in place).
+    Returns a NormOut; ``sinv`` goes with the codes to ``mm`` or ``mm_act``
+    (a scale per row to ``mm_act`` only).
+    """
+    f32 = _gamma_checked(gamma, x)
+    rows, cols = x.shape
+    _same(residual, x, "residual")
+    if residual is not None:
+        if h is None:
+            h = torch.empty_like(x)
+        else:
+            _same(h, x, "h")
+    elif h is not None:
+        raise ValueError("h needs a residual: without one it is x")
+    if y is not None:
+        _same(y, x, "y")
+    elif need_y or fmt is None:
+        y = torch.empty_like(x)
+    rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if need_rstd else None
+    sinv = row_sinv = None
+    if fmt is None:
+        if ring is not None or codes is not None or amax is not None:
+            raise ValueError("codes, ring and amax need fmt")
+    else:
+        if codes is None:
+            codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        else:
+            _same(codes, x, "codes", None, torch.uint8)
+        _scalar(amax, x, "amax")
+        if ring is not None:
+            _ring_on(ring, x, "ring")
+            sinv = ring.scale_inv
+        elif amax is not None:
+            raise ValueError("amax needs a ring")
+        else:
+            sinv = row_sinv = torch.empty(rows, dtype=torch.float32, device=x.device)
+    a = CNormArgs(x.data_ptr(), _ptr(residual), IN_DTYPE[x.dtype], rows, cols, gamma.data_ptr(), f32, eps, _ptr(h),
+                  _ptr(y), _ptr(rstd), _ptr(codes), fmt or 0, ring.c() if ring is not None else _NO_RING, _ptr(amax),
+                  _ptr(row_sinv))
+    _check((_LIB or lib()).fp8_rmsnorm(ctypes.byref(a), _raw_stream(x.get_device())), "fp8_rmsnorm")
+    return NormOut(codes, sinv, x if h is None else h, rstd, y)
+
+
+class CNormBwdArgs(ctypes.Structure):
+    """Mirror of ``fp8_rmsnorm_backward_args``."""
+
+    _fields_ = [("dy", ctypes.c_void_p), ("h", ctypes.c_void_p), ("dres", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("rstd", ctypes.c_void_p),
+                ("gamma", ctypes.c_void_p), ("gamma_f32", ctypes.c_int), ("dx", ctypes.c_void_p),
+                ("dgamma", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+@_on_stream
+def rmsnorm_backward(dy, h, rstd, gamma, dres=None, dx=None, need_dgamma=True):
+    """fp8_rmsnorm_backward: (dx, dgamma) of ``rmsnorm`` from its h and rstd.
+
+    dx [rows, cols] is the gradient of x and of residual alike; dres is the
+    gradient that reaches h past the norm.  dy, h, dres and dx have one type;
+    dx may be dy or dres (in place).  dgamma is float32 [cols], or None.
+    """
+    f32 = _gamma_checked(gamma, h)
+    rows, cols = h.shape
+    _same(dy, h, "dy")
+    _same(dres, h, "dres")
+    _same(rstd, h, "rstd", (rows,), torch.float32)
+    if dx is None:
+        dx = torch.empty_like(h)
+    else:
+        _same(dx, h, "dx")
+    L = _LIB or lib()
+    dgamma = ws = None
+    wsb = 0
+    if need_dgamma:
+        dgamma = torch.empty(cols, dtype=torch.float32, device=h.device)
+        wsb = L.fp8_rmsnorm_backward_workspace_bytes(rows, cols)
+        if wsb:
+            ws = torch.empty(wsb, dtype=torch.uint8, device=h.device)
+    a = CNormBwdArgs(dy.data_ptr(), h.data_ptr(), _ptr(dres), IN_DTYPE[h.dtype], rows, cols, rstd.data_ptr(),
+                     gamma.data_ptr(), f32, dx.data_ptr(), _ptr(dgamma), _ptr(ws), wsb)
+    _check(L.fp8_rmsnorm_backward(ctypes.byref(a), _raw_stream(h.get_device())), "fp8_rmsnorm_backward")
+    return dx, dgamma
 
 
 WAIT_BUDGET_DEFAULT_NS = 2_000_000_000

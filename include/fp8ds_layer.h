@@ -1,0 +1,113 @@
+/*
+ * fp8ds_layer.h -- C ABI of the operators around the FP8 linear: the norm that
+ * feeds it, the product with an activation in its epilogue, and the gradients
+ * of both.
+ *
+ * Conventions as fp8ds.h: caller-owned device memory, asynchronous on the
+ * caller's stream and the current device, negative fp8_status on an error,
+ * every argument checked on the host before anything is launched.
+ */
+#ifndef FP8DS_LAYER_H_
+#define FP8DS_LAYER_H_
+
+#include "fp8ds.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * fp8_rmsnorm -- root-mean-square norm with the residual's addition and an
+ * FP8 output.  Per row of cols values, sums in float32:
+ *   h = x + residual, rounded once to x's type (h = x without a residual);
+ *       everything below reads the rounded h, the value the stream keeps
+ *   r = 1 / sqrt(mean(h^2) + eps)
+ *   v = (h * r) * gamma                     (float32)
+ * and, of these outputs, those that are wanted:
+ *   h      the residual stream, x's type (required with a residual)
+ *   rstd   r, float32 [rows], what the backward needs
+ *   y      v rounded to x's type
+ *   codes  FP8 codes [rows, cols]:
+ *          row_sinv NULL: saturate_rne(fp32(v * s)) with s = *ring.scale read
+ *          at launch; ring folds amax = max |v| (NaN ignored) exactly as
+ *          fp8_quantize folds its input's, in the same launch.  With amax_out
+ *          set the ring's history, idx and scale are left alone: the launch
+ *          writes amax there and 1/s to ring.scale_inv (as
+ *          fp8_quantize_local; fp8_ring_fold folds later).
+ *          row_sinv set: every row has its own current scale, FP8_MAX / max |v|
+ *          of the row (1 when that is 0 or not finite); row_sinv[r] = 1/scale
+ *          is what fp8_mm_act takes as a row-wise sinv_a.  ring is unused.
+ *          Rows on their own scales suit serving: a call keeps no state.
+ *
+ * x, residual, h, y  [rows, cols] row-major, contiguous, element type dtype
+ *         (fp8_in_dtype), any address aligned to the element.  h or y may be
+ *         x or residual itself (in place).  Otherwise no output may overlap
+ *         another argument.
+ * gamma   [cols], of x's type or float32 (gamma_f32 != 0).
+ * rows >= 0 (0 still folds amax 0 into a ring), 1 <= cols <= 16384, eps > 0.
+ * Errors: FP8_ERR_INVALID_ARG (bad enum, negative size, cols 0, eps not
+ *         positive and finite, NULL x or gamma, a residual without h, h
+ *         without a residual, no output at all, codes without a complete ring
+ *         or row_sinv, ring arguments without codes, a ring with row_sinv,
+ *         an output that overlaps another argument);
+ *         FP8_ERR_UNSUPPORTED (cols above 16384, rows above 2^31, an address
+ *         not aligned to its element, ring.scratch not 8-byte aligned).
+ */
+typedef struct {
+  const void* x;
+  const void* residual; /* NULL: h = x */
+  int dtype;
+  int64_t rows, cols;
+  const void* gamma;
+  int gamma_f32;
+  float eps;
+  void* h;
+  void* y;
+  float* rstd;
+  uint8_t* codes;
+  int fmt;
+  fp8_ring ring;
+  float* amax_out;
+  float* row_sinv;
+} fp8_rmsnorm_args;
+int fp8_rmsnorm(const fp8_rmsnorm_args* args, fp8_stream_t stream);
+
+/*
+ * fp8_rmsnorm_backward -- the gradient of fp8_rmsnorm, with the codes' cast
+ * taken as the identity.  With n = h * rstd and g = dy * gamma (float32):
+ *   dx     = dres + rstd * (g - n * mean(g * n)), rounded once to h's type:
+ *            the gradient of x and, the same values, of residual.  dres is the
+ *            gradient that reaches h past the norm (NULL: none).
+ *   dgamma = sum over rows of dy * n, float32 [cols] (NULL: not wanted).  The
+ *            order of the sums depends on rows, cols and the device only, so
+ *            repeated calls give the same bits.
+ * dy, h, dres, dx  [rows, cols], contiguous, element type dtype; dx may be dy
+ *         or dres itself.
+ * workspace  at least fp8_rmsnorm_backward_workspace_bytes(rows, cols) bytes,
+ *         4-byte aligned, no initial value; unused (may be NULL) without
+ *         dgamma.  Calls that may overlap on the GPU need one each.
+ * Errors as fp8_rmsnorm; FP8_ERR_INVALID_ARG also for a workspace that is
+ *         missing or too small.  rows == 0 sets dgamma to 0.
+ */
+typedef struct {
+  const void* dy;
+  const void* h;
+  const void* dres;
+  int dtype;
+  int64_t rows, cols;
+  const float* rstd;
+  const void* gamma;
+  int gamma_f32;
+  void* dx;
+  float* dgamma;
+  void* workspace;
+  size_t workspace_bytes;
+} fp8_rmsnorm_backward_args;
+int fp8_rmsnorm_backward(const fp8_rmsnorm_backward_args* args, fp8_stream_t stream);
+size_t fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FP8DS_LAYER_H_ */
