@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "amax_fold.cuh"
+#include "colsum.cuh"
 #include "common.cuh"
 #include "elem_io.cuh"
 #include "fp8_ring.cuh"
@@ -298,29 +299,6 @@ __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(const __grid_constant__
   }
 }
 
-// out[c] = sum over p of partial[p][c], p ascending within each of the 32
-// warps of a block and the warps' sums in order.
-__global__ void __launch_bounds__(1024) colsum_kernel(const float* partial, int n, int cols, float* out) {
-  __shared__ float s[32][33];
-  pdl_launch_dependents();
-  pdl_wait_prior_grid();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float acc = 0.0f;
-  if (c < cols) {
-#pragma unroll 8
-    for (int p = warp; p < n; p += 32) acc += partial[int64_t(p) * cols + c];
-  }
-  s[warp][lane] = acc;
-  __syncthreads();
-  if (warp == 0 && c < cols) {
-    float r = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 32; ++w) r += s[w][lane];
-    out[c] = r;
-  }
-}
-
 // ---- host side -----------------------------------------------------------------
 
 // How a row is split: W = 2^log_w warps and V vectors per thread.
@@ -516,9 +494,7 @@ extern "C" int fp8_rmsnorm_backward(const fp8_rmsnorm_backward_args* p, fp8_stre
   a.log_w = s.log_w;
   a.dx = static_cast<uint8_t*>(p->dx);
   if (p->rows == 0) {  // no rows: the empty sum
-    const cudaError_t e = launch_pdl(colsum_kernel, dim3(unsigned((p->cols + 31) / 32)), dim3(1024), 0, st, 1,
-                                     static_cast<const float*>(nullptr), 0, a.cols, p->dgamma);
-    return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+    return launch_colsum(nullptr, 0, p->cols, p->dgamma, st);
   }
   if (p->dgamma != nullptr) {
     if (grid > 1) {
@@ -536,7 +512,5 @@ extern "C" int fp8_rmsnorm_backward(const fp8_rmsnorm_backward_args* p, fp8_stre
     default: r = al ? launch_bwd<FP8_IN_FP32, true>(a, s, grid, st) : launch_bwd<FP8_IN_FP32, false>(a, s, grid, st); break;
   }
   if (r != FP8_OK || p->dgamma == nullptr || grid == 1) return r;
-  const cudaError_t e = launch_pdl(colsum_kernel, dim3(unsigned((p->cols + 31) / 32)), dim3(1024), 0, st, 1,
-                                   static_cast<const float*>(a.partial), int(grid), a.cols, p->dgamma);
-  return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+  return launch_colsum(a.partial, int(grid), p->cols, p->dgamma, st);
 }

@@ -110,6 +110,10 @@ def lib():
         L.fp8_rmsnorm_backward.restype = i32
         L.fp8_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
         L.fp8_rmsnorm_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.fp8_act_backward.argtypes = [vp, vp]
+        L.fp8_act_backward.restype = i32
+        L.fp8_act_backward_workspace_bytes.argtypes = [i64, i64, i32]
+        L.fp8_act_backward_workspace_bytes.restype = ctypes.c_size_t
         L.fp8_launch_count.argtypes = []
         L.fp8_launch_count.restype = ctypes.c_uint64
         _LIB = L
@@ -767,6 +771,70 @@ def rmsnorm_backward(dy, h, rstd, gamma, dres=None, dx=None, need_dgamma=True):
                      gamma.data_ptr(), f32, dx.data_ptr(), _ptr(dgamma), _ptr(ws), wsb)
     _check(L.fp8_rmsnorm_backward(ctypes.byref(a), _raw_stream(h.get_device())), "fp8_rmsnorm_backward")
     return dx, dgamma
+
+
+class CActBwdArgs(ctypes.Structure):
+    """Mirror of ``fp8_act_backward_args``."""
+
+    _fields_ = [("dy", ctypes.c_void_p), ("dtype", ctypes.c_int), ("z", ctypes.c_void_p), ("u", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("act", ctypes.c_int), ("fmt", ctypes.c_int),
+                ("ring", CRing), ("ring_u", CRing), ("amax_out", ctypes.c_void_p), ("amax_out_u", ctypes.c_void_p),
+                ("dzq", ctypes.c_void_p), ("duq", ctypes.c_void_p), ("db", ctypes.c_void_p), ("dbu", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class ActGrad(NamedTuple):
+    """What ``act_backward`` returns; what was not asked for is None."""
+
+    dz: torch.Tensor             # uint8 codes [rows, cols], dequantised by ring.scale_inv
+    du: Optional[torch.Tensor]   # uint8 codes, dequantised by ring_u.scale_inv
+    db: Optional[torch.Tensor]   # float32 [cols], column sums of dz
+    dbu: Optional[torch.Tensor]  # float32 [cols], column sums of du
+
+
+@_on_stream
+def act_backward(dy, z, act, fmt, ring, u=None, ring_u=None, need_db=False, amax=None, amax_u=None):
+    """fp8_act_backward: the gradient of ``mm_act``'s epilogue as FP8 codes.
+
+    dy: contiguous 2-D CUDA tensor (bf16/fp16/fp32); z: the bf16 pre-activation
+    that ``mm_act`` saved; u: the bf16 operand that it multiplied by (AUX_MUL),
+    with ring_u for u's gradient.  dz = dy [u] act'(z) and du = dy act(z) are
+    cast to fmt on the rings' delayed scales, which are folded in the same
+    launch (or, with amax / amax_u, left to ``ring_fold``).  need_db adds the
+    column sums of dz (and du): the bias gradients.  With ACT_NONE and
+    without u, z may be None.  Returns an ActGrad.
+    """
+    if dy.dtype not in IN_DTYPE:
+        raise ValueError(f"{dy.dtype} is not one of bfloat16, float16, float32")
+    if dy.dim() != 2 or not dy.is_contiguous():
+        raise ValueError("dy must be a contiguous 2-D tensor")
+    rows, cols = dy.shape
+    _same(z, dy, "z", None, torch.bfloat16)
+    _same(u, dy, "u", None, torch.bfloat16)
+    if (u is None) != (ring_u is None):
+        raise ValueError("u and ring_u go together")
+    _ring_on(ring, dy, "ring")
+    _ring_on(ring_u, dy, "ring_u")
+    _scalar(amax, dy, "amax")
+    _scalar(amax_u, dy, "amax_u")
+    dev = dy.device
+    L = _LIB or lib()
+    dz = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+    du = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if u is not None else None
+    db = dbu = ws = None
+    wsb = 0
+    if need_db:
+        db = torch.empty(cols, dtype=torch.float32, device=dev)
+        if u is not None:
+            dbu = torch.empty(cols, dtype=torch.float32, device=dev)
+        wsb = L.fp8_act_backward_workspace_bytes(rows, cols, 0 if u is None else 1)
+        if wsb:
+            ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
+    a = CActBwdArgs(dy.data_ptr(), IN_DTYPE[dy.dtype], _ptr(z), _ptr(u), rows, cols, act, fmt, ring.c(),
+                    ring_u.c() if ring_u is not None else _NO_RING, _ptr(amax), _ptr(amax_u), dz.data_ptr(), _ptr(du),
+                    _ptr(db), _ptr(dbu), _ptr(ws), wsb)
+    _check(L.fp8_act_backward(ctypes.byref(a), _raw_stream(dy.get_device())), "fp8_act_backward")
+    return ActGrad(dz, du, db, dbu)
 
 
 WAIT_BUDGET_DEFAULT_NS = 2_000_000_000

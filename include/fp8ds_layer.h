@@ -106,6 +106,63 @@ typedef struct {
 int fp8_rmsnorm_backward(const fp8_rmsnorm_backward_args* args, fp8_stream_t stream);
 size_t fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
 
+/* Activations of fp8_mm_act and fp8_act_backward: value and slope at z.
+ *   RELU  max(z, 0), slope 1 for z > 0, else 0
+ *   GELU  the tanh form: z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
+ *   SILU  z / (1 + e^-z) */
+typedef enum { FP8_ACT_NONE = 0, FP8_ACT_RELU = 1, FP8_ACT_GELU = 2, FP8_ACT_SILU = 3 } fp8_act;
+
+/*
+ * fp8_act_backward -- the gradient of fp8_mm_act's epilogue, cast to FP8 for
+ * the backward products.  In float32, per element of [rows, cols]:
+ *   without u:  dz = dy * act'(z)
+ *   with u:     dz = dy * u * act'(z),  du = dy * act(z)
+ *               (y = act(z) * u, the gated form)
+ *   dzq    FP8 codes of dz on ring's delayed scale; ring folds max |dz| in the
+ *          same launch, exactly as fp8_quantize folds its input's.  What
+ *          fp8_mm's backward products take as the output gradient.
+ *   duq    the same of du with ring_u (required with u).
+ *   db     column sums of dz, float32 [cols], or NULL: the bias gradient.
+ *   dbu    column sums of du, or NULL (needs u and db).
+ * amax_out / amax_out_u set: that ring is left to fp8_ring_fold, as in
+ * fp8_quantize_local.  The gradient of an added residual is dy itself.
+ *
+ * dy      [rows, cols] contiguous, element type dtype (fp8_in_dtype).
+ * z, u    [rows, cols] contiguous bf16: the pre-activation that fp8_mm_act
+ *         saved, and the operand it multiplied by.  With FP8_ACT_NONE and no
+ *         u, z may be NULL: a cast of dy that also gives the bias gradient.
+ * The sums' order depends on rows, cols and the device only: repeated calls
+ * give the same bits.  workspace: at least
+ * fp8_act_backward_workspace_bytes(rows, cols, gated) bytes, 4-byte aligned,
+ * no initial value; unused without db.  Calls that may overlap need one each.
+ * rows, cols >= 0; an empty call still folds amax 0, and sets db to 0.
+ * Errors: FP8_ERR_INVALID_ARG (bad enum, negative size, a missing or
+ *         superfluous pointer, one ring for both outputs, a workspace that is
+ *         missing or too small, an output that overlaps another argument);
+ *         FP8_ERR_UNSUPPORTED (an address not aligned to its element, a ring's
+ *         scratch not 8-byte aligned, cols above 2^30, rows above 2^31).
+ */
+typedef struct {
+  const void* dy;
+  int dtype;
+  const void* z;
+  const void* u;
+  int64_t rows, cols;
+  int act;
+  int fmt;
+  fp8_ring ring, ring_u;
+  float* amax_out;
+  float* amax_out_u;
+  uint8_t* dzq;
+  uint8_t* duq;
+  float* db;
+  float* dbu;
+  void* workspace;
+  size_t workspace_bytes;
+} fp8_act_backward_args;
+int fp8_act_backward(const fp8_act_backward_args* args, fp8_stream_t stream);
+size_t fp8_act_backward_workspace_bytes(int64_t rows, int64_t cols, int gated);
+
 #ifdef __cplusplus
 }
 #endif

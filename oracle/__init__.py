@@ -38,10 +38,11 @@ Modules:
                  FP8 output codes and of the output amax.
   bias_grad   -- column sums of the output gradient (the bias gradient).
   norm        -- root-mean-square norm, its per-row scales and its gradient.
+  act         -- activations of the product, their slopes and the gradient of its epilogue.
 
 Parity status: every function is pinned by ``tests/test_oracle_*.py``
 except the treatment of NaN inputs and of a non-finite history maximum,
 which no workload exercises ("parity unpinned" for those two cases).
 """
 
-from . import fp8_formats, recipe, gemm, bias_grad, norm  # noqa: F401
+from . import fp8_formats, recipe, gemm, bias_grad, norm, act  # noqa: F401

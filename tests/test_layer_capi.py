@@ -85,3 +85,27 @@ def test_binding_refuses_cpu_tensors():
     for call in (lambda: ops.rmsnorm(x, g), lambda: ops.rmsnorm_backward(x, x, torch.ones(2), g)):
         with pytest.raises(ValueError):
             call()
+
+
+def _act_bwd(L, **kw):
+    f = dict(dy=0x100000, dtype=0, z=0x200000, u=None, rows=4, cols=16, act=3, fmt=1, ring=_ring(), ring_u=ops.CRing(),
+             amax_out=None, amax_out_u=None, dzq=0x400000, duq=None, db=None, dbu=None, workspace=None,
+             workspace_bytes=0)
+    f.update(kw)
+    return L.fp8_act_backward(ctypes.byref(ops.CActBwdArgs(*f.values())), None)
+
+
+def test_act_backward_refusals(L):
+    assert L.fp8_act_backward(None, None) == BAD
+    gate = dict(u=0x300000, ring_u=_ring(0xA00000), duq=0x500000)
+    for kw in (dict(dtype=3), dict(rows=-1), dict(cols=-1), dict(act=4), dict(act=-1), dict(fmt=2), dict(dy=None),
+               dict(z=None), dict(act=0, z=None, **gate), dict(dzq=None), dict(ring=ops.CRing()),
+               dict(u=0x300000), dict(u=0x300000, duq=0x500000), dict(ring_u=_ring(0xA00000)), dict(duq=0x500000),
+               dict(gate, ring_u=_ring()), dict(dbu=0x600000), dict(gate, dbu=0x600000), dict(dbu=0x600000, db=0x700000),
+               dict(amax_out_u=0x700000), dict(dzq=0x100000), dict(gate, duq=0x400010), dict(db=0x100000),
+               dict(db=0x600000, workspace=0x600010, workspace_bytes=64)):
+        assert _act_bwd(L, **kw) == BAD, kw
+    for kw in (dict(cols=(1 << 30) + 1), dict(rows=1 << 31), dict(dy=0x100001), dict(dtype=2, dy=0x100002),
+               dict(z=0x200001), dict(gate, u=0x300001), dict(db=0x600002),
+               dict(ring=ops.CRing(0x900000, 0x900040, 0x900044, 0x900048, 0x90004C))):
+        assert _act_bwd(L, **kw) == UNSUP, kw
