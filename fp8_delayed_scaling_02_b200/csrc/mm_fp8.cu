@@ -38,8 +38,11 @@
 #include <cstring>
 #include <mutex>
 
+#include "activation.cuh"
 #include "common.cuh"
 #include "fp8_ring.cuh"
+#include "fp8ds_layer.h"
+#include "host_util.cuh"
 
 namespace fp8ds {
 namespace {
@@ -115,10 +118,18 @@ struct MmParams {
   float* r_scale_inv;
   uint32_t* r_scratch;  // [0] amax bits, [1] CTA ticket; zero between calls
   float* amax_out;      // data-parallel shard: the amax goes here, no fold
+  // Activation epilogue: y = act(z) [+ or * aux], z optionally kept.
+  int act;
+  int a_rows;           // sinv_a holds one factor per row of A
+  const uint16_t* aux;  // bf16 [M, N], added (aux_mul 0) or multiplied
+  int aux_mul;
+  uint16_t* z;          // bf16 [M, N], or null
+  int z_tma;            // z leaves through TMA stores (tmZ valid)
 };
 
 constexpr int kEpiOut8 = 1;   // EPI bit: FP8 output codes + output ring fold
 constexpr int kEpiBias8 = 2;  // EPI bit: FP8 bias codes
+constexpr int kEpiAct = 4;    // EPI bit: activation, residual or gate operand, kept pre-activation
 
 // Value of one FP8 code (exact in fp32; NaN codes give NaN).
 __device__ __forceinline__ float fp8_value(uint8_t c, int fmt) {
@@ -447,10 +458,11 @@ __device__ __forceinline__ void decode_tile(const MmParams& p, int t, int& b, in
 // CTA (pair) `cta` of the `ctas` that work on this problem.
 template <int BN, int PAIR, int EPI>
 __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMap* tmB, const CUtensorMap* tmC,
-                                        const MmParams& p, const int cta, const int ctas) {
+                                        const CUtensorMap* tmZ, const MmParams& p, const int cta, const int ctas) {
   using C = Cfg<BN, PAIR>;
   constexpr bool kOut8 = (EPI & kEpiOut8) != 0;
   constexpr bool kBias8 = (EPI & kEpiBias8) != 0;
+  constexpr bool kAct = (EPI & kEpiAct) != 0;
   constexpr int kTileM = kBM * PAIR;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment for the swizzled tiles (the same offset in both CTAs of a pair).
@@ -647,7 +659,7 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
     const int quad = warp & 3;
     const int half = ew >> 2;
     constexpr int kHalfCols = BN / 2;
-    const float sab = __fmul_rn(*p.sinv_a, *p.sinv_b);
+    float sab = __fmul_rn(*p.sinv_a, *p.sinv_b);  // with a factor per row: set per tile
     const float bsc = kBias8 ? *p.bias_scale : 0.0f;  // FP8 bias dequantisation factor
     const float s_out = kOut8 ? *p.r_scale : 0.0f;    // FP8 output: the output ring's scale
     float amax = 0.0f;                                 // FP8 output: max |y| of this lane's elements
@@ -707,6 +719,9 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
       const int m0 = mt * kTileM + int(rank) * kBM + quad * 32;
       const uint32_t tbase = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * kHalfCols);
       const int nbase = nt * BN + half * kHalfCols;
+      if constexpr (kAct) {
+        if (p.a_rows) sab = m0 + lane < p.M ? __fmul_rn(__ldg(p.sinv_a + m0 + lane), *p.sinv_b) : 0.0f;
+      }
       // This warp's bias, four columns per lane (lane l: nbase + 4l .. 4l+3),
       // read once per tile; emit() takes a chunk's 32 values from 8 lanes by
       // shuffle.  (Broadcast loads of the same values in every chunk cost a
@@ -735,27 +750,151 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
         if (lane == 0) mbar_arrive_cluster(release_bar);
         released = true;
       };
+      // Bias of columns n0 + 4j .. n0 + 4j + 3.
+      auto bias_of = [&](int n0, int j) {
+        const int src = ((n0 - nbase) >> 5) * 8 + j;
+        float4 bv;
+        bv.x = __shfl_sync(0xFFFFFFFFu, bias_l.x, src);
+        bv.y = __shfl_sync(0xFFFFFFFFu, bias_l.y, src);
+        bv.z = __shfl_sync(0xFFFFFFFFu, bias_l.z, src);
+        bv.w = __shfl_sync(0xFFFFFFFFu, bias_l.w, src);
+        return bv;
+      };
+      // A 32 x 32 bf16 chunk at columns n0, this lane's row in packed[0, 16).
+      // (With an activation, z and y may leave in different ways from the
+      // same buffers: every use of a buffer commits a group, an empty one
+      // where no TMA store was issued, so that "at most one group pending"
+      // always means that the buffer's last store has read it.)
+      auto store_bf16 = [&](int n0, const uint32_t(&packed)[16], const CUtensorMap* tm, uint16_t* base, bool tma) {
+        const uint32_t sbuf = stage0 + uint32_t(buf) * kStagingBytes;
+        // The buffer's previous TMA store has read it (checked after the math,
+        // so the wait overlaps it).
+        if ((tma || kAct) && lane == 0) bulk_wait_read_le1();
+        __syncwarp();
+        // 16-byte unit u of this lane's 64-byte row holds columns 8u .. 8u+7,
+        // at unit position u ^ ((lane >> 1) & 3).
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t addr = sbuf + uint32_t(lane) * 64u + uint32_t((u ^ ((lane >> 1) & 3)) * 16);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(packed[4 * u]),
+                       "r"(packed[4 * u + 1]), "r"(packed[4 * u + 2]), "r"(packed[4 * u + 3])
+                       : "memory");
+        }
+        if (tma) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(tm, sbuf, n0, m0, b);
+            bulk_commit();
+          }
+        } else {
+          // Rows not 16-byte aligned: the chunk staged in the same swizzled
+          // layout is written row by row, lane l taking column n0 + l, so
+          // each store instruction covers 64 contiguous bytes.
+          __syncwarp();
+          const bool col_ok = n0 + lane < p.N;
+          uint16_t* obase = base + int64_t(b) * p.c_stride + int64_t(m0) * p.N + n0 + lane;
+#pragma unroll 4
+          for (int rr = 0; rr < 32; ++rr) {
+            const uint32_t addr = sbuf + uint32_t(rr) * 64u + uint32_t((((lane >> 3) ^ ((rr >> 1) & 3)) << 4)) +
+                                  uint32_t((lane & 7) << 1);
+            uint16_t v16;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v16) : "r"(addr) : "memory");
+            if (col_ok && m0 + rr < p.M) obase[int64_t(rr) * p.N] = v16;
+          }
+          if (kAct && lane == 0) bulk_commit();
+        }
+        buf ^= 1;
+      };
+      // Activation epilogue of a chunk: v, accumulators in, becomes y.
+      auto act_chunk = [&](int n0, uint32_t(&v)[32]) {
+        uint32_t aux[16];
+        if (p.aux != nullptr) {
+          // Read row by row, lane l taking column n0 + l (64 contiguous bytes
+          // per load, any alignment), turned through a staging buffer.
+          const uint32_t sbuf = stage0 + uint32_t(buf) * kStagingBytes;
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+          const bool col_ok = n0 + lane < p.N;
+          const uint16_t* abase = p.aux + int64_t(m0) * p.N + n0 + lane;
+#pragma unroll 16
+          for (int rr = 0; rr < 32; ++rr) {
+            const uint16_t a16 = col_ok && m0 + rr < p.M ? abase[int64_t(rr) * p.N] : uint16_t(0);
+            const uint32_t addr = sbuf + uint32_t(rr) * 64u + uint32_t((((lane >> 3) ^ ((rr >> 1) & 3)) << 4)) +
+                                  uint32_t((lane & 7) << 1);
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(a16) : "memory");
+          }
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t addr = sbuf + uint32_t(lane) * 64u + uint32_t((u ^ ((lane >> 1) & 3)) * 16);
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(aux[4 * u]), "=r"(aux[4 * u + 1]), "=r"(aux[4 * u + 2]), "=r"(aux[4 * u + 3])
+                         : "r"(addr)
+                         : "memory");
+          }
+          __syncwarp();
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (has_bias) bv = bias_of(n0, j);
+          float* y = reinterpret_cast<float*>(v + 4 * j);
+          fma2(y[0], y[1], sab, bv.x, bv.y);
+          fma2(y[2], y[3], sab, bv.z, bv.w);
+        }
+        float* y = reinterpret_cast<float*>(v);
+        if (p.z != nullptr) {
+          uint32_t zp[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+            zp[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          store_bf16(n0, zp, tmZ, p.z, p.z_tma != 0);
+        }
+        switch (p.act) {  // warp-uniform
+          case FP8_ACT_RELU:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = act_value(FP8_ACT_RELU, y[j]);
+            break;
+          case FP8_ACT_GELU:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = act_value(FP8_ACT_GELU, y[j]);
+            break;
+          case FP8_ACT_SILU:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = act_value(FP8_ACT_SILU, y[j]);
+            break;
+          default: break;
+        }
+        if (p.aux != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float lo = __uint_as_float(aux[j] << 16), hi = __uint_as_float(aux[j] & 0xFFFF0000u);
+            y[2 * j] = p.aux_mul ? __fmul_rn(y[2 * j], lo) : __fadd_rn(y[2 * j], lo);
+            y[2 * j + 1] = p.aux_mul ? __fmul_rn(y[2 * j + 1], hi) : __fadd_rn(y[2 * j + 1], hi);
+          }
+        }
+      };
       // One 32 x 32 chunk at output columns n0 (this lane's row): scale, bias,
       // one bf16 rounding, store.
-      auto emit = [&](int n0, const uint32_t(&v)[32]) {
+      auto emit = [&](int n0, uint32_t(&v)[32]) {
         if (m0 >= p.M) return;  // warp-uniform: rows beyond M (pair peer of a short last tile)
+        if constexpr (kAct) act_chunk(n0, v);
         const bool full = n0 + 32 <= p.N;
         const bool row_ok = m0 + lane < p.M;
         uint32_t packed[16];  // bf16 pairs, or (FP8 output) code quads in [0, 8)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (has_bias) {  // warp-uniform
-            const int src = ((n0 - nbase) >> 5) * 8 + j;
-            bv.x = __shfl_sync(0xFFFFFFFFu, bias_l.x, src);
-            bv.y = __shfl_sync(0xFFFFFFFFu, bias_l.y, src);
-            bv.z = __shfl_sync(0xFFFFFFFFu, bias_l.z, src);
-            bv.w = __shfl_sync(0xFFFFFFFFu, bias_l.w, src);
-          }
+          if (!kAct && has_bias) bv = bias_of(n0, j);
           float y0 = __uint_as_float(v[4 * j + 0]), y1 = __uint_as_float(v[4 * j + 1]);
           float y2 = __uint_as_float(v[4 * j + 2]), y3 = __uint_as_float(v[4 * j + 3]);
-          fma2(y0, y1, sab, bv.x, bv.y);  // acc * sinv_a*sinv_b + bias, one rounding each
-          fma2(y2, y3, sab, bv.z, bv.w);
+          if constexpr (!kAct) {
+            fma2(y0, y1, sab, bv.x, bv.y);  // acc * sinv_a*sinv_b + bias, one rounding each
+            fma2(y2, y3, sab, bv.z, bv.w);
+          }
           if constexpr (kOut8) {
             // amax over this lane's in-range elements (NaN ignored), then the
             // codes of y * s_out.
@@ -805,6 +944,7 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
           // layout, then written row by row, lane l taking column n0 + l, so
           // each store instruction covers 32 contiguous bytes of one row.
           const uint32_t sbuf = stage0 + uint32_t(buf) * kStagingBytes;
+          if (kAct && lane == 0) bulk_wait_read_le1();
           __syncwarp();  // every lane has read this buffer's previous chunk
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -824,47 +964,11 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
             asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v16) : "r"(addr) : "memory");
             if (col_ok && m0 + rr < p.M) obase[int64_t(rr) * p.N] = uint8_t(v16);
           }
+          if (kAct && lane == 0) bulk_commit();
           buf ^= 1;
           return;
         }
-        const uint32_t sbuf = stage0 + uint32_t(buf) * kStagingBytes;
-        // The buffer's previous TMA store has read it (checked after the math,
-        // so the wait overlaps it).
-        if (p.tma_store && lane == 0) bulk_wait_read_le1();
-        __syncwarp();
-        // 16-byte unit u of this lane's 64-byte row holds columns 8u .. 8u+7,
-        // at unit position u ^ ((lane >> 1) & 3).
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t addr = sbuf + uint32_t(lane) * 64u + uint32_t((u ^ ((lane >> 1) & 3)) * 16);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(packed[4 * u]),
-                       "r"(packed[4 * u + 1]), "r"(packed[4 * u + 2]), "r"(packed[4 * u + 3])
-                       : "memory");
-        }
-        if (p.tma_store) {
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(tmC, sbuf, n0, m0, b);
-            bulk_commit();
-          }
-        } else {
-          // Rows not 16-byte aligned: the chunk staged in the same swizzled
-          // layout is written row by row, lane l taking column n0 + l, so
-          // each store instruction covers 64 contiguous bytes.
-          __syncwarp();
-          const bool col_ok = n0 + lane < p.N;
-          uint16_t* obase = p.out + int64_t(b) * p.c_stride + int64_t(m0) * p.N + n0 + lane;
-#pragma unroll 4
-          for (int rr = 0; rr < 32; ++rr) {
-            const uint32_t addr = sbuf + uint32_t(rr) * 64u + uint32_t((((lane >> 3) ^ ((rr >> 1) & 3)) << 4)) +
-                                  uint32_t((lane & 7) << 1);
-            uint16_t v16;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v16) : "r"(addr) : "memory");
-            if (col_ok && m0 + rr < p.M) obase[int64_t(rr) * p.N] = v16;
-          }
-        }
-        buf ^= 1;
+        store_bf16(n0, packed, tmC, p.out, p.tma_store);
       };
       auto add4 = [](uint32_t* v, const float4& w) {
         v[0] = __float_as_uint(__uint_as_float(v[0]) + w.x);
@@ -950,7 +1054,7 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
     }
     // The staging buffers are released once the stores have read them; waiting
     // for the global writes too kept every CTA alive ~0.4 us longer.
-    if (p.tma_store && lane == 0) bulk_wait_read_all();
+    if ((p.tma_store || kAct) && lane == 0) bulk_wait_read_all();
     __syncwarp();
   }
 
@@ -978,7 +1082,16 @@ template <int BN, int PAIR, int EPI>
 __global__ void __launch_bounds__(kThreadsMM, 1)
     mm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ MmParams p) {
-  mm_body<BN, PAIR, EPI>(&tmA, &tmB, &tmC, p, int(blockIdx.x) / PAIR, int(gridDim.x) / PAIR);
+  mm_body<BN, PAIR, EPI>(&tmA, &tmB, &tmC, nullptr, p, int(blockIdx.x) / PAIR, int(gridDim.x) / PAIR);
+}
+
+// The product with an activation epilogue.
+template <int BN, int PAIR, int EPI>
+__global__ void __launch_bounds__(kThreadsMM, 1)
+    mm_act_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmZ,
+                  const __grid_constant__ MmParams p) {
+  mm_body<BN, PAIR, EPI | kEpiAct>(&tmA, &tmB, &tmC, &tmZ, p, int(blockIdx.x) / PAIR, int(gridDim.x) / PAIR);
 }
 
 // Two independent GEMMs in one persistent launch (the dX and dW GEMMs of a
@@ -992,8 +1105,8 @@ __global__ void __launch_bounds__(kThreadsMM, 1)
                        const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
                        const __grid_constant__ CUtensorMap tmC1, const __grid_constant__ MmParams p1, const int split) {
   const int g = int(blockIdx.x) / PAIR;
-  if (g < split) mm_body<BN, PAIR, 0>(&tmA0, &tmB0, &tmC0, p0, g, split);
-  else mm_body<BN, PAIR, 0>(&tmA1, &tmB1, &tmC1, p1, g - split, int(gridDim.x) / PAIR - split);
+  if (g < split) mm_body<BN, PAIR, 0>(&tmA0, &tmB0, &tmC0, nullptr, p0, g, split);
+  else mm_body<BN, PAIR, 0>(&tmA1, &tmB1, &tmC1, nullptr, p1, g - split, int(gridDim.x) / PAIR - split);
 }
 
 // K == 0: Y = bf16(bias) or 0.
@@ -1030,6 +1143,48 @@ __global__ void __launch_bounds__(256) mm_out8_small_kernel(const MmParams p, in
     amax = fmaxf(amax, fabsf(y));
     p.out8[b * p.c_stride + r] = p.out_fmt == FP8_E5M2 ? cvt_one<FP8_E5M2>(y, s) : cvt_one<FP8_E4M3>(y, s);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  float a = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) a = fmaxf(a, warp_max[w]);
+  if (p.amax_out != nullptr) {
+    *p.amax_out = a;
+    *p.r_scale_inv = __frcp_rn(s);
+    return;
+  }
+  float hist[kHistoryLen];
+#pragma unroll
+  for (int i = 0; i < kHistoryLen; ++i) hist[i] = p.r_history[i];
+  if (p.out_fmt == FP8_E5M2)
+    ring_commit<FP8_E5M2>(a, hist, *p.r_idx, p.r_history, p.r_idx, p.r_scale, p.r_scale_inv, s);
+  else
+    ring_commit<FP8_E4M3>(a, hist, *p.r_idx, p.r_history, p.r_idx, p.r_scale, p.r_scale_inv, s);
+}
+
+// K == 0 with an activation: z = bias.  One CTA, like mm_out8_small_kernel.
+__global__ void __launch_bounds__(256) mm_act_k0_kernel(const MmParams p, int64_t M, int64_t N) {
+  __shared__ float warp_max[8];
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  const float s = p.out8 != nullptr ? *p.r_scale : 1.0f;
+  float amax = 0.0f;
+  for (int64_t i = threadIdx.x; i < M * N; i += blockDim.x) {
+    const float z = bias_at(p, i % N);
+    if (p.z != nullptr) p.z[i] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
+    float y = act_value(p.act, z);
+    if (p.aux != nullptr) {
+      const float x = __uint_as_float(uint32_t(p.aux[i]) << 16);
+      y = p.aux_mul ? __fmul_rn(y, x) : __fadd_rn(y, x);
+    }
+    amax = fmaxf(amax, fabsf(y));
+    if (p.out8 != nullptr) p.out8[i] = p.out_fmt == FP8_E5M2 ? cvt_one<FP8_E5M2>(y, s) : cvt_one<FP8_E4M3>(y, s);
+    else p.out[i] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+  }
+  if (p.out8 == nullptr) return;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
@@ -1234,6 +1389,33 @@ int launch_mm(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t 
     case kEpiBias8: return launch_mm_epi<BN, PAIR, kEpiBias8>(A, B, M, N, K, batch, strides, p, c, ws, st);
     default: return launch_mm_epi<BN, PAIR, kEpiOut8 | kEpiBias8>(A, B, M, N, K, batch, strides, p, c, ws, st);
   }
+}
+
+template <int BN, int PAIR, int EPI>
+int launch_act_epi(const MmProblem& q, const MmChoice& c, cudaStream_t st) {
+  CUtensorMap ta, tb, tc, tz;
+  MmParams p = q.p;
+  const int rc = prepare_mm<BN, PAIR>(q.A, q.B, q.M, q.N, q.K, 1, nullptr, p, c, nullptr, ta, tb, tc);
+  if (rc != FP8_OK) return rc;
+  memset(&tz, 0, sizeof(tz));
+  if (p.z_tma && !make_out_map(&tz, p.z, q.M, q.N, 1, q.M * q.N)) return FP8_ERR_CUDA;
+  static bool done[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8_ERR_CUDA;
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(mm_act_kernel<BN, PAIR, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<BN, PAIR>::kSmemBytes) != cudaSuccess)
+      return FP8_ERR_CUDA;
+    done[dev] = true;
+  }
+  const cudaError_t e = launch_pdl(mm_act_kernel<BN, PAIR, EPI>, dim3(PAIR * std::max(1, c.grid)), dim3(kThreadsMM),
+                                   Cfg<BN, PAIR>::kSmemBytes, st, PAIR, ta, tb, tc, tz, p);
+  return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+}
+
+template <int BN, int PAIR>
+int launch_act(const MmProblem& q, const MmChoice& c, cudaStream_t st) {
+  return q.epi & kEpiOut8 ? launch_act_epi<BN, PAIR, kEpiOut8>(q, c, st) : launch_act_epi<BN, PAIR, 0>(q, c, st);
 }
 
 template <int BN, int PAIR>
@@ -1585,4 +1767,48 @@ extern "C" size_t fp8_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_
   if (sms <= 0) return 0;
   const MmChoice c = choose_mm(M, N, K, batch, sms, (layout & FP8_MM_B_MN_MAJOR) != 0, size_t(1) << 40);
   return c.ws_bytes;
+}
+
+extern "C" int fp8_mm_act(const fp8_mm_act_args* a, fp8_stream_t stream) {
+  if (a == nullptr) return FP8_ERR_INVALID_ARG;
+  if (a->act < FP8_ACT_NONE || a->act > FP8_ACT_SILU) return FP8_ERR_INVALID_ARG;
+  if (a->aux_op != FP8_AUX_ADD && a->aux_op != FP8_AUX_MUL) return FP8_ERR_INVALID_ARG;
+  if ((a->layout & ~(FP8_MM_A_E5M2 | FP8_MM_B_E5M2)) != FP8_MM_NT) return FP8_ERR_INVALID_ARG;
+  const bool out8 = a->out_kind != FP8_MM_OUT_BF16;
+  MmEpilogue ex{nullptr, nullptr, a->out_kind, out8 ? static_cast<uint8_t*>(a->out) : nullptr, a->out_ring, a->out_amax};
+  MmProblem q;
+  const int rc = mm_validate(a->A, a->B, a->M, a->N, a->K, 1, nullptr, a->layout, a->sinv_a, a->sinv_b, a->bias,
+                             out8 ? nullptr : static_cast<uint16_t*>(a->out), q, &ex);
+  if (rc != FP8_OK) return rc;
+  if (!on(a->aux, 2) || !on(a->z, 2) || !on(a->sinv_a, 4) || !on(a->sinv_b, 4) || !on(a->bias, 4))
+    return FP8_ERR_UNSUPPORTED;
+  const size_t mn = size_t(a->M) * size_t(a->N);
+  const Span spans[] = {{a->A, size_t(a->M) * size_t(a->K), false, false, false},
+                        {a->B, size_t(a->N) * size_t(a->K), false, false, false},
+                        {a->sinv_a, a->sinv_a_rows ? size_t(a->M) * 4 : 4, false, false, false},
+                        {a->sinv_b, 4, false, false, false},
+                        {a->bias, size_t(a->N) * 4, false, false, false},
+                        {a->aux, mn * 2, false, false, true},
+                        {a->z, mn * 2, true, false, false},
+                        {a->out, mn * (out8 ? 1 : 2), true, true, false}};
+  if (!q.nothing && spans_clash(spans, 8)) return FP8_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (q.nothing) return out8 ? launch_out8_small(q, st) : FP8_OK;
+  MmParams& p = q.p;
+  p.act = a->act;
+  p.a_rows = a->sinv_a_rows != 0;
+  p.aux = a->aux;
+  p.aux_mul = a->aux_op == FP8_AUX_MUL;
+  p.z = a->z;
+  p.z_tma = a->z != nullptr && on(a->z, 16) && a->N % 8 == 0;
+  if (q.K == 0)
+    return launch_pdl(mm_act_k0_kernel, dim3(1), dim3(256), 0, st, 1, p, q.M, q.N) == cudaSuccess ? FP8_OK
+                                                                                                 : FP8_ERR_CUDA;
+  const int sms = sm_count();
+  if (sms <= 0) return FP8_ERR_CUDA;
+  const MmChoice c = choose_mm(q.M, q.N, q.K, 1, sms, false, 0);
+  if (c.pair == 2) return launch_act<256, 2>(q, c, st);
+  if (c.bn == 256) return launch_act<256, 1>(q, c, st);
+  if (c.bn == 128) return launch_act<128, 1>(q, c, st);
+  return launch_act<64, 1>(q, c, st);
 }

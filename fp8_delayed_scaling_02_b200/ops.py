@@ -114,6 +114,8 @@ def lib():
         L.fp8_act_backward.restype = i32
         L.fp8_act_backward_workspace_bytes.argtypes = [i64, i64, i32]
         L.fp8_act_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.fp8_mm_act.argtypes = [vp, vp]
+        L.fp8_mm_act.restype = i32
         L.fp8_launch_count.argtypes = []
         L.fp8_launch_count.restype = ctypes.c_uint64
         _LIB = L
@@ -771,6 +773,71 @@ def rmsnorm_backward(dy, h, rstd, gamma, dres=None, dx=None, need_dgamma=True):
                      gamma.data_ptr(), f32, dx.data_ptr(), _ptr(dgamma), _ptr(ws), wsb)
     _check(L.fp8_rmsnorm_backward(ctypes.byref(a), _raw_stream(h.get_device())), "fp8_rmsnorm_backward")
     return dx, dgamma
+
+
+class CMmActArgs(ctypes.Structure):
+    """Mirror of ``fp8_mm_act_args``."""
+
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("layout", ctypes.c_int), ("sinv_a", ctypes.c_void_p),
+                ("sinv_a_rows", ctypes.c_int), ("sinv_b", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("act", ctypes.c_int), ("aux", ctypes.c_void_p), ("aux_op", ctypes.c_int), ("z", ctypes.c_void_p),
+                ("out_kind", ctypes.c_int), ("out", ctypes.c_void_p), ("out_ring", CRing),
+                ("out_amax", ctypes.c_void_p)]
+
+
+@_on_stream
+def mm_act(a, b, sinv_a, sinv_b, act=ACT_NONE, bias=None, aux=None, aux_op=AUX_ADD, need_z=False, out_fmt=None,
+           out_ring=None, out_amax=None, fmt_a=E4M3, fmt_b=E4M3, out=None, z=None):
+    """fp8_mm_act: z = A . B^T * sinv_a * sinv_b + bias, y = act(z) [+ or * aux].
+
+    a: uint8 codes [M, K], b: uint8 codes [N, K]; sinv_a: a float32 CUDA tensor
+    of one element or of M (a factor per row, ``rmsnorm``'s sinv without a
+    ring); sinv_b: of one.  bias: float32 [N]; aux: bf16 [M, N], added
+    (AUX_ADD: a residual) or multiplied (AUX_MUL: a gate).  out_fmt None gives
+    bf16 [M, N]; E4M3 / E5M2 give codes on out_ring's delayed scale, folded in
+    the same launch (or, with out_amax, left to ``ring_fold``).  need_z keeps z
+    in bf16 for ``act_backward``.  out may be aux (in place).
+    Returns (out, z); z is None when not asked for.
+    """
+    if a.dtype != torch.uint8 or b.dtype != torch.uint8 or a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a and b are 2-D uint8 FP8 codes")
+    (M, K), (N, Kb) = a.shape, b.shape
+    if Kb != K:
+        raise ValueError("K mismatch")
+    if not a.is_contiguous() or not b.is_contiguous() or b.device != a.device:
+        raise ValueError("a and b must be contiguous, on one device")
+    na = sinv_a.numel()
+    if na != 1 and na != M:
+        raise ValueError(f"sinv_a has {na} elements, expected 1 or {M}")
+    _same(sinv_a, a, "sinv_a", sinv_a.shape, torch.float32)
+    _scalar(sinv_b, a, "sinv_b")
+    _same(bias, a, "bias", (N,), torch.float32)
+    _same(aux, a, "aux", (M, N), torch.bfloat16)
+    _scalar(out_amax, a, "out_amax")
+    if out_fmt is None:
+        if out_ring is not None or out_amax is not None:
+            raise ValueError("out_ring and out_amax need out_fmt")
+        kind, dtype = MM_OUT_BF16, torch.bfloat16
+    else:
+        if out_ring is None:
+            raise ValueError("an FP8 output needs out_ring")
+        _ring_on(out_ring, a, "out_ring")
+        kind, dtype = (MM_OUT_E4M3 if out_fmt == E4M3 else MM_OUT_E5M2 if out_fmt == E5M2 else -1), torch.uint8
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=a.device)
+    else:
+        _same(out, a, "out", (M, N), dtype)
+    if z is not None:
+        _same(z, a, "z", (M, N), torch.bfloat16)
+    elif need_z:
+        z = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+    args = CMmActArgs(a.data_ptr(), b.data_ptr(), M, N, K,
+                      (MM_A_E5M2 if fmt_a == E5M2 else 0) | (MM_B_E5M2 if fmt_b == E5M2 else 0), sinv_a.data_ptr(),
+                      1 if na != 1 else 0, sinv_b.data_ptr(), _ptr(bias), act, _ptr(aux), aux_op, _ptr(z), kind,
+                      out.data_ptr(), out_ring.c() if out_ring is not None else _NO_RING, _ptr(out_amax))
+    _check((_LIB or lib()).fp8_mm_act(ctypes.byref(args), _raw_stream(a.get_device())), "fp8_mm_act")
+    return out, z
 
 
 class CActBwdArgs(ctypes.Structure):

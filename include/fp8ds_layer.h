@@ -112,6 +112,53 @@ size_t fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *   SILU  z / (1 + e^-z) */
 typedef enum { FP8_ACT_NONE = 0, FP8_ACT_RELU = 1, FP8_ACT_GELU = 2, FP8_ACT_SILU = 3 } fp8_act;
 
+/* What fp8_mm_act does with its bf16 operand: y = act(z) + aux, or act(z) * aux. */
+typedef enum { FP8_AUX_ADD = 0, FP8_AUX_MUL = 1 } fp8_aux_op;
+
+/*
+ * fp8_mm_act -- the scaled FP8 product with an activation, and a residual or a
+ * gate, in its epilogue.  In float32, for m in [0, M), n in [0, N):
+ *   z[m,n] = fp32_acc(sum_k A[m,k] B[n,k]) * (sinv_a * sinv_b) + bias[n]
+ *            (one fused multiply-add, as fp8_mm)
+ *   t = act(z);  y = t, t + aux[m,n] or t * aux[m,n]
+ * and rounded once from there:
+ *   z      bf16 [M, N], or NULL: the pre-activation for fp8_act_backward
+ *   out    out_kind FP8_MM_OUT_BF16: bf16 [M, N]; FP8_MM_OUT_E4M3 / _E5M2: FP8
+ *          codes of fp32(y * s), s = *out_ring.scale read at launch, with
+ *          max |y| folded into out_ring (or written to out_amax) as fp8_mm_ex.
+ *
+ * A, B    FP8 codes [M, K] and [N, K], K contiguous; layout: FP8_MM_A_E5M2 and
+ *         FP8_MM_B_E5M2 only.
+ * sinv_a  one float, or (sinv_a_rows != 0) M floats: a factor per row of A, as
+ *         fp8_rmsnorm's row_sinv gives them.
+ * bias    float32 [N] or NULL.  aux: bf16 [M, N] or NULL.  All contiguous.
+ *         out may be aux itself (a residual stream updated in place).
+ * M, N >= 0, K >= 0 with K % 16 == 0; K == 0 gives z = bias; an empty output
+ * still folds amax 0.
+ * Errors as fp8_mm_ex; FP8_ERR_INVALID_ARG also for an unknown act or aux_op,
+ *         other layout bits, an output that overlaps another argument;
+ *         FP8_ERR_UNSUPPORTED for an address not aligned to its element.
+ */
+typedef struct {
+  const uint8_t* A;
+  const uint8_t* B;
+  int64_t M, N, K;
+  int layout;
+  const float* sinv_a;
+  int sinv_a_rows;
+  const float* sinv_b;
+  const float* bias;
+  int act;
+  const uint16_t* aux;
+  int aux_op;
+  uint16_t* z;
+  int out_kind;
+  void* out;
+  fp8_ring out_ring;
+  float* out_amax;
+} fp8_mm_act_args;
+int fp8_mm_act(const fp8_mm_act_args* args, fp8_stream_t stream);
+
 /*
  * fp8_act_backward -- the gradient of fp8_mm_act's epilogue, cast to FP8 for
  * the backward products.  In float32, per element of [rows, cols]:

@@ -109,3 +109,25 @@ def test_act_backward_refusals(L):
                dict(z=0x200001), dict(gate, u=0x300001), dict(db=0x600002),
                dict(ring=ops.CRing(0x900000, 0x900040, 0x900044, 0x900048, 0x90004C))):
         assert _act_bwd(L, **kw) == UNSUP, kw
+
+
+def _mm_act(L, **kw):
+    f = dict(A=0x100000, B=0x200000, M=128, N=128, K=128, layout=0, sinv_a=0x300000, sinv_a_rows=0, sinv_b=0x310000,
+             bias=None, act=1, aux=None, aux_op=0, z=None, out_kind=0, out=0x400000, out_ring=ops.CRing(), out_amax=None)
+    f.update(kw)
+    return L.fp8_mm_act(ctypes.byref(ops.CMmActArgs(*f.values())), None)
+
+
+def test_mm_act_refusals(L):
+    assert L.fp8_mm_act(None, None) == BAD
+    for kw in (dict(M=-1), dict(N=-1), dict(K=-16), dict(layout=1), dict(layout=2), dict(layout=1 << 10), dict(act=4),
+               dict(act=-1), dict(aux_op=2), dict(out_kind=3), dict(out_kind=1), dict(out=None), dict(A=None),
+               dict(sinv_a=None), dict(sinv_b=None), dict(out_amax=0x500000), dict(z=0x400100), dict(out=0x100000),
+               dict(aux=0x500000, z=0x500000), dict(aux=0x500000, out=0x500002),
+               dict(out_kind=1, out=0x500000, aux=0x500000, out_ring=_ring())):
+        assert _mm_act(L, **kw) == BAD, kw
+    for kw in (dict(K=24), dict(A=0x100008), dict(B=0x200001), dict(out=0x400001), dict(aux=0x500001), dict(z=0x500001),
+               dict(bias=0x500002), dict(sinv_a=0x300002),
+               dict(out_kind=1, out_ring=ops.CRing(0x900000, 0x900040, 0x900044, 0x900048, 0x90004C))):
+        assert _mm_act(L, **kw) == UNSUP, kw
+    assert _mm_act(L, M=0) == ops.FP8_OK
