@@ -13,6 +13,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "fp8_ring.cuh"
 #include "fp8ds_layer.h"
 
 namespace fp8ds {
@@ -64,6 +65,81 @@ __device__ __forceinline__ void act_value_slope(int act, float z, float& value, 
     default:
       value = z;
       slope = 1.0f;
+  }
+}
+
+// ---- two values at a time, for the product's epilogue ------------------------
+//
+// There the eight epilogue warps have about 36 issue slots per element while
+// the next tile's products run, so each operation that can is a packed one and
+// one reciprocal serves two values: 1/x = y r, 1/y = x r with r = 1/(x y).
+// z is held at or above a floor first (-41 for silu, -7.4 for gelu, where the
+// value is within 2^-53 of 0), so that x and y stay below 2^60: no overflow,
+// and a huge negative z gives 0.
+
+__device__ __forceinline__ void mul2(float& a, float& b, float c, float d) {
+  asm("{\n\t.reg .b64 ra, rc;\n\t"
+      "mov.b64 ra, {%0, %1};\n\t"
+      "mov.b64 rc, {%2, %3};\n\t"
+      "mul.rn.f32x2 ra, ra, rc;\n\t"
+      "mov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+  asm("{\n\t.reg .b64 ra, rc;\n\t"
+      "mov.b64 ra, {%0, %1};\n\t"
+      "mov.b64 rc, {%2, %3};\n\t"
+      "add.rn.f32x2 ra, ra, rc;\n\t"
+      "mov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+constexpr float kLog2E = 1.4426950408889634f;
+
+template <int ACT>
+__device__ __forceinline__ void act_pair(float& a, float& b) {
+  if constexpr (ACT == FP8_ACT_RELU) {
+    a = max_nan(a, 0.0f);
+    b = max_nan(b, 0.0f);
+  } else {
+    constexpr bool kGelu = ACT == FP8_ACT_GELU;
+    a = max_nan(a, kGelu ? -7.4f : -41.0f);
+    b = max_nan(b, kGelu ? -7.4f : -41.0f);
+    float x = a, y = b;  // -> 2^(-w log2 e) + 1
+    if constexpr (kGelu) {
+      constexpr float c1 = -kGeluC2 * kLog2E;
+      mul2(x, y, a, b);
+      fma2(x, y, c1 * kGeluA, c1, c1);
+      mul2(x, y, a, b);
+    } else {
+      scale2(x, y, -kLog2E);
+    }
+    x = exp2_fast(x);
+    y = exp2_fast(y);
+    add2(x, y, 1.0f, 1.0f);
+    const float r = rcp_fast(x * y);
+    mul2(a, b, r * y, r * x);
   }
 }
 

@@ -28,6 +28,7 @@ enum WaitSite : uint32_t {
   kWaitDrain = 5,
   kWaitQuantizeTma = 6,
   kWaitSplitK = 7,
+  kWaitEpilogueAux = 8,
 };
 
 // Library-global device error word (defined in capi.cu, relocatable device code

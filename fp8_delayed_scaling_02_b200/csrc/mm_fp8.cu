@@ -37,6 +37,7 @@
 #include <algorithm>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "common.cuh"
@@ -71,6 +72,22 @@ struct Cfg {
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static_assert((2 * kStages + 5) * 8 + 16 + 4 * kEpiWarps + 8 <= 256,
                 "barrier area: barriers, TMEM slot, abort, amax, stall barrier");
+};
+
+// The same with an activation epilogue, whose warps each have four buffers for
+// the operand that turns into the output in place (two loads ahead, one in
+// work, one leaving) and two for the kept pre-activation: four stages are left
+// of six on CTA pairs, which still cover a load's way from L2.
+constexpr int kActBufs = 4, kActZBufs = 2;
+template <int BN, int PAIR>
+struct ActCfg : Cfg<BN, PAIR> {
+  using B = Cfg<BN, PAIR>;
+  static constexpr int kWarpStaging = (kActBufs + kActZBufs) * kStagingBytes;
+  static constexpr int kStages = (232448 - 512 - 1024 - kEpiWarps * kWarpStaging) / B::kStageBytes;
+  static constexpr int kStagingOffset = kStages * B::kStageBytes;
+  static constexpr int kBarOffset = kStagingOffset + kEpiWarps * kWarpStaging;
+  static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
+  static_assert(kSmemBytes <= 232448 && kStages >= 2, "shared memory budget");
 };
 
 struct MmParams {
@@ -121,8 +138,9 @@ struct MmParams {
   // Activation epilogue: y = act(z) [+ or * aux], z optionally kept.
   int act;
   int a_rows;           // sinv_a holds one factor per row of A
-  const uint16_t* aux;  // bf16 [M, N], added (aux_mul 0) or multiplied
+  const uint16_t* aux;  // bf16 [M, N], added (aux_mul 0) or multiplied, or null
   int aux_mul;
+  int aux_tma;          // aux comes through TMA loads (tmX valid)
   uint16_t* z;          // bf16 [M, N], or null
   int z_tma;            // z leaves through TMA stores (tmZ valid)
 };
@@ -246,6 +264,9 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, uint32_t src
                    reinterpret_cast<uint64_t>(tm)),
                "r"(src), "r"(c0), "r"(c1), "r"(c2)
                : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read_le1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
@@ -454,15 +475,292 @@ __device__ __forceinline__ void decode_tile(const MmParams& p, int t, int& b, in
   nt = rr / gm;
 }
 
+// ---- activation epilogue -----------------------------------------------------------
+//
+// y = act(z) [+ or * aux] for z = acc * sinv + bias, by the eight epilogue
+// warps of a CTA, each a 32-row quadrant by half the tile's columns in chunks
+// of 32 x 32.  Per chunk: TMEM -> z; z in bf16 to a z buffer; act; the aux
+// chunk, which a TMA load has put into the chunk's buffer; the result over it
+// in place; one group of TMA stores for z and y.  The load for the chunk after
+// next is issued as each chunk begins, across tiles, into the buffer whose
+// store is two groups back, so neither its latency nor a store's is waited for.
+// Tensors whose rows are not 16-byte multiples go through the same buffers by
+// guarded accesses, 64 contiguous bytes of one row per warp access.
+
+struct ActTile {
+  int i, chunks, m0, nbase;  // tile ordinal of this CTA, valid chunks, first row and column of this warp
+};
+
+template <int BN, int PAIR>
+__device__ __forceinline__ bool act_tile(const MmParams& p, int cta, int ctas, uint32_t rank, int quad, int half, int i,
+                                         ActTile& t) {
+  const int tile = cta + i * ctas;
+  if (tile >= p.dp_tiles) return false;
+  int b, mt, nt;
+  decode_tile(p, tile, b, mt, nt);
+  t.i = i;
+  t.m0 = mt * kBM * PAIR + int(rank) * kBM + quad * 32;
+  t.nbase = nt * BN + half * (BN / 2);
+  t.chunks = t.m0 >= p.M || t.nbase >= p.N ? 0 : min(BN / 64, (p.N - t.nbase + 31) / 32);
+  return true;
+}
+
+// act(y) of a chunk, two elements at a time.
+template <int ACT>
+__device__ __forceinline__ void act_chunk(float (&y)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) act_pair<ACT>(y[j], y[j + 1]);
+}
+
+// 16-byte unit u of row r of a 32 x 32 bf16 buffer (TMA's 64-byte swizzle).
+__device__ __forceinline__ uint32_t unit64(uint32_t buf, int r, int u) {
+  return buf + uint32_t(r) * 64u + uint32_t((u ^ ((r >> 1) & 3)) * 16);
+}
+
+template <int BN, int PAIR, bool kOut8>
+__device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUtensorMap* tmX, const CUtensorMap* tmZ,
+                                              const MmParams& p, const int cta, const int ctas, const uint32_t rank,
+                                              const int ew, const int quad, const int lane, const uint32_t staging,
+                                              const uint32_t tmem_base, const uint32_t bar0, volatile int* abort) {
+  using C = ActCfg<BN, PAIR>;
+  const int half = ew >> 2;
+  const uint32_t tfull0 = bar0 + 8u * (2 * C::kStages), tempty0 = tfull0 + 16u;
+  const uint32_t stall_bar = bar0 + 8u * (2 * C::kStages + 11);
+  const uint32_t aux_bar = bar0 + 256u + 8u * (kActBufs * ew);
+  const uint32_t bufs = staging + uint32_t(ew) * C::kWarpStaging, zbufs = bufs + kActBufs * kStagingBytes;
+  const float sinv_b = *p.sinv_b;
+  const float sab_all = __fmul_rn(*p.sinv_a, sinv_b);
+  const float s_out = kOut8 ? *p.r_scale : 0.0f;
+  const bool prefetch = p.aux != nullptr && p.aux_tma;
+  float amax = 0.0f;
+
+  // The next aux chunk to ask for: chunk `pc` of tile `pt`, number `pq` in this warp's sequence.
+  ActTile pt{-1, 0, 0, 0};
+  int pc = 0;
+  uint32_t pq = 0;
+  bool more = prefetch;
+  auto ask = [&]() {  // warp-uniform; lane 0 issues
+    while (more && pc >= pt.chunks) {
+      pc = 0;
+      more = act_tile<BN, PAIR>(p, cta, ctas, rank, quad, half, pt.i + 1, pt);
+    }
+    if (!more) return;
+    if (lane == 0) {
+      const uint32_t b = pq & (kActBufs - 1);
+      mbar_arrive_expect_tx(aux_bar + 8u * b, kStagingBytes);
+      tma_load_3d(bufs + b * kStagingBytes, tmX, pt.nbase + 32 * pc, pt.m0, 0, aux_bar + 8u * b);
+    }
+    ++pc;
+    ++pq;
+  };
+  ask();
+  ask();
+
+  uint32_t q = 0;  // chunks done
+  bool ok = true;
+  ActTile t;
+  for (int i = 0; ok && act_tile<BN, PAIR>(p, cta, ctas, rank, quad, half, i, t); ++i) {
+    const int acc = i & 1;
+    // (Testing: with the stall site set here, the wait is on a barrier that
+    // nothing completes, so it runs out and the abort path runs.)
+    const bool stall = p.stall == kWaitEpilogueTmemFull;
+    if (!mbar_wait(stall ? stall_bar : tfull0 + 8u * acc, stall ? 0u : (i >> 1) & 1, abort, p.err,
+                   kWaitEpilogueTmemFull, p.wait_ns))
+      break;
+    tc_fence_after();
+    const uint32_t release_bar = PAIR == 1 ? tempty0 + 8u * acc : mapa_shared(tempty0 + 8u * acc, 0);
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(release_bar);
+    };
+    if (t.chunks == 0) {
+      release();
+      continue;
+    }
+    const uint32_t tbase = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * (BN / 2));
+    const int m = t.m0 + lane;
+    const bool row_ok = m < p.M;
+    float sab = sab_all;
+    if (p.a_rows) sab = row_ok ? __fmul_rn(__ldg(p.sinv_a + m), sinv_b) : 0.0f;
+    // Bias of columns nbase + 4 lane .. + 3, read once per tile, handed out by shuffle.
+    float4 bias_l = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.bias != nullptr && lane < BN / 8) {
+      const int c4 = t.nbase + 4 * lane;
+      bias_l.x = c4 < p.N ? __ldg(p.bias + c4) : 0.f;
+      bias_l.y = c4 + 1 < p.N ? __ldg(p.bias + c4 + 1) : 0.f;
+      bias_l.z = c4 + 2 < p.N ? __ldg(p.bias + c4 + 2) : 0.f;
+      bias_l.w = c4 + 3 < p.N ? __ldg(p.bias + c4 + 3) : 0.f;
+    }
+#pragma unroll 1
+    for (int c = 0; c < t.chunks; ++c, ++q) {
+      const int n0 = t.nbase + 32 * c;
+      const uint32_t buf = bufs + (q & (kActBufs - 1)) * kStagingBytes;
+      const uint32_t zbuf = zbufs + (q & (kActZBufs - 1)) * kStagingBytes;
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld32_nowait(tbase + uint32_t(32 * c), r);
+      // One group per chunk: with at most one pending, the stores of the chunk
+      // two back have read their buffers, which the next load and z reuse.
+      if (lane == 0) bulk_wait_read_le1();
+      __syncwarp();
+      ask();
+      uint32_t aux[16];
+      if (p.aux != nullptr) {
+        if (p.aux_tma) {
+          if (!mbar_wait(aux_bar + 8u * (q & (kActBufs - 1)), (q / kActBufs) & 1, abort, p.err, kWaitEpilogueAux,
+                         p.wait_ns)) {
+            ok = false;
+          }
+          ok = __all_sync(0xFFFFFFFFu, ok);
+        } else {
+          const bool col_ok = n0 + lane < p.N;
+          const uint16_t* src = p.aux + int64_t(t.m0) * p.N + n0 + lane;
+#pragma unroll 16
+          for (int rr = 0; rr < 32; ++rr) {
+            const uint16_t a16 = col_ok && t.m0 + rr < p.M ? src[int64_t(rr) * p.N] : uint16_t(0);
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(unit64(buf, rr, lane >> 3) + uint32_t((lane & 7) << 1)),
+                         "h"(a16)
+                         : "memory");
+          }
+          __syncwarp();
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(aux[4 * u]), "=r"(aux[4 * u + 1]), "=r"(aux[4 * u + 2]), "=r"(aux[4 * u + 3])
+                       : "r"(unit64(buf, lane, u))
+                       : "memory");
+      }
+      tmem_wait_ld();
+      if (c + 1 == t.chunks) release();
+      if (!ok) break;
+      float y[32];
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.bias != nullptr) {  // warp-uniform
+          const int src = 8 * c + j / 4;
+          bv.x = __shfl_sync(0xFFFFFFFFu, bias_l.x, src);
+          bv.y = __shfl_sync(0xFFFFFFFFu, bias_l.y, src);
+          bv.z = __shfl_sync(0xFFFFFFFFu, bias_l.z, src);
+          bv.w = __shfl_sync(0xFFFFFFFFu, bias_l.w, src);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[j + e] = __uint_as_float(r[j + e]);
+        fma2(y[j], y[j + 1], sab, bv.x, bv.y);
+        fma2(y[j + 2], y[j + 3], sab, bv.z, bv.w);
+      }
+      auto pack = [&](int j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(y[j], y[j + 1]);
+        return *reinterpret_cast<const uint32_t*>(&h);
+      };
+      if (p.z != nullptr) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          st_shared16(unit64(zbuf, lane, u), pack(8 * u), pack(8 * u + 2), pack(8 * u + 4), pack(8 * u + 6));
+      }
+      switch (p.act) {  // warp-uniform
+        case FP8_ACT_RELU: act_chunk<FP8_ACT_RELU>(y); break;
+        case FP8_ACT_GELU: act_chunk<FP8_ACT_GELU>(y); break;
+        case FP8_ACT_SILU: act_chunk<FP8_ACT_SILU>(y); break;
+        default: break;
+      }
+      if (p.aux != nullptr) {
+        if (p.aux_mul) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            mul2(y[2 * j], y[2 * j + 1], __uint_as_float(aux[j] << 16), __uint_as_float(aux[j] & 0xFFFF0000u));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            add2(y[2 * j], y[2 * j + 1], __uint_as_float(aux[j] << 16), __uint_as_float(aux[j] & 0xFFFF0000u));
+        }
+      }
+      if constexpr (kOut8) {
+        // Columns beyond N hold act(0) and aux 0, hence y = 0; rows beyond M do not count.
+        if (row_ok) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) amax = fmaxf(amax, fmaxf(fabsf(y[j]), fabsf(y[j + 1])));
+        }
+        uint32_t code[8];
+        if (p.out_fmt == FP8_E5M2) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) code[j] = cvt4<FP8_E5M2>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) code[j] = cvt4<FP8_E4M3>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out);
+        }
+        // 32 x 32 codes in the first 1 KB, 32B swizzle: 16-byte unit u of row
+        // r at unit u ^ ((r >> 2) & 1).  They lie over other lanes' aux rows.
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          st_shared16(buf + uint32_t(lane) * 32u + uint32_t((u ^ ((lane >> 2) & 1)) * 16), code[4 * u], code[4 * u + 1],
+                      code[4 * u + 2], code[4 * u + 3]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          st_shared16(unit64(buf, lane, u), pack(8 * u), pack(8 * u + 2), pack(8 * u + 4), pack(8 * u + 6));
+      }
+      if (!p.tma_store || (p.z != nullptr && !p.z_tma)) {
+        // Rows that TMA cannot write: lane l takes column n0 + l of every row.
+        __syncwarp();
+        const bool col_ok = n0 + lane < p.N;
+        const int64_t o = int64_t(t.m0) * p.N + n0 + lane;
+#pragma unroll 4
+        for (int rr = 0; rr < 32; ++rr) {
+          if (!col_ok || t.m0 + rr >= p.M) continue;
+          uint16_t v;
+          if (p.z != nullptr && !p.z_tma) {
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(unit64(zbuf, rr, lane >> 3) + uint32_t((lane & 7) << 1)) : "memory");
+            p.z[o + int64_t(rr) * p.N] = v;
+          }
+          if (!p.tma_store) {
+            if constexpr (kOut8) {
+              asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(buf + uint32_t(rr) * 32u + uint32_t((((lane >> 4) ^ ((rr >> 2) & 1)) << 4) + (lane & 15))) : "memory");
+              p.out8[o + int64_t(rr) * p.N] = uint8_t(v);
+            } else {
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(unit64(buf, rr, lane >> 3) + uint32_t((lane & 7) << 1)) : "memory");
+              p.out[o + int64_t(rr) * p.N] = v;
+            }
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (p.z != nullptr && p.z_tma) tma_store_3d(tmZ, zbuf, n0, t.m0, 0);
+        if (p.tma_store) tma_store_3d(tmC, buf, n0, t.m0, 0);
+        bulk_commit();
+      }
+    }
+  }
+  if (lane == 0) {
+    // Loads asked for and not consumed (only after a wait gave up) land before
+    // shared memory is released; stores have read it.
+    for (; q < pq; ++q) {
+      const unsigned long long t0 = globaltimer_ns();
+      while (!mbar_try_wait(aux_bar + 8u * (q & (kActBufs - 1)), (q / kActBufs) & 1) &&
+             globaltimer_ns() - t0 < kWaitBudgetNs) {
+      }
+    }
+    bulk_wait_read_all();
+  }
+  __syncwarp();
+  return amax;
+}
+
 // One CTA's (pair's) whole life: problem `p` with maps tmA / tmB / tmC, as
 // CTA (pair) `cta` of the `ctas` that work on this problem.
 template <int BN, int PAIR, int EPI>
 __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMap* tmB, const CUtensorMap* tmC,
-                                        const CUtensorMap* tmZ, const MmParams& p, const int cta, const int ctas) {
-  using C = Cfg<BN, PAIR>;
+                                        const MmParams& p, const int cta, const int ctas,
+                                        const CUtensorMap* tmX = nullptr, const CUtensorMap* tmZ = nullptr) {
+  constexpr bool kAct = (EPI & kEpiAct) != 0;
+  using C = std::conditional_t<kAct, ActCfg<BN, PAIR>, Cfg<BN, PAIR>>;
   constexpr bool kOut8 = (EPI & kEpiOut8) != 0;
   constexpr bool kBias8 = (EPI & kEpiBias8) != 0;
-  constexpr bool kAct = (EPI & kEpiAct) != 0;
   constexpr int kTileM = kBM * PAIR;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment for the swizzled tiles (the same offset in both CTAs of a pair).
@@ -500,6 +798,9 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
     }
     mbar_init(done_bar, 1);
     mbar_init(stall_bar, 1);
+    if constexpr (kAct) {
+      for (int k = 0; k < kActBufs * kEpiWarps; ++k) mbar_init(bar0 + 256u + 8u * k, 1);
+    }
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -646,6 +947,15 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
       }
     }
     __syncwarp();
+  } else if constexpr (kAct) {
+    const float amax_l = act_epilogue<BN, PAIR, kOut8>(tmC, tmX, tmZ, p, cta, ctas, rank, warp - 2, warp & 3, lane,
+                                                       sbase + C::kStagingOffset, tmem_base, bar0, abort);
+    if constexpr (kOut8) {
+      float amax = amax_l;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+      if (lane == 0) amax_s[warp - 2] = amax;
+    }
   } else {
     // ---------------- epilogue (warps 2..9 of each CTA) ----------------
     // Warp w reads TMEM lane quadrant w % 4 (rows 32*(w%4) .. +31 of this
@@ -659,7 +969,7 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
     const int quad = warp & 3;
     const int half = ew >> 2;
     constexpr int kHalfCols = BN / 2;
-    float sab = __fmul_rn(*p.sinv_a, *p.sinv_b);  // with a factor per row: set per tile
+    const float sab = __fmul_rn(*p.sinv_a, *p.sinv_b);
     const float bsc = kBias8 ? *p.bias_scale : 0.0f;  // FP8 bias dequantisation factor
     const float s_out = kOut8 ? *p.r_scale : 0.0f;    // FP8 output: the output ring's scale
     float amax = 0.0f;                                 // FP8 output: max |y| of this lane's elements
@@ -719,9 +1029,6 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
       const int m0 = mt * kTileM + int(rank) * kBM + quad * 32;
       const uint32_t tbase = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * kHalfCols);
       const int nbase = nt * BN + half * kHalfCols;
-      if constexpr (kAct) {
-        if (p.a_rows) sab = m0 + lane < p.M ? __fmul_rn(__ldg(p.sinv_a + m0 + lane), *p.sinv_b) : 0.0f;
-      }
       // This warp's bias, four columns per lane (lane l: nbase + 4l .. 4l+3),
       // read once per tile; emit() takes a chunk's 32 values from 8 lanes by
       // shuffle.  (Broadcast loads of the same values in every chunk cost a
@@ -750,151 +1057,27 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
         if (lane == 0) mbar_arrive_cluster(release_bar);
         released = true;
       };
-      // Bias of columns n0 + 4j .. n0 + 4j + 3.
-      auto bias_of = [&](int n0, int j) {
-        const int src = ((n0 - nbase) >> 5) * 8 + j;
-        float4 bv;
-        bv.x = __shfl_sync(0xFFFFFFFFu, bias_l.x, src);
-        bv.y = __shfl_sync(0xFFFFFFFFu, bias_l.y, src);
-        bv.z = __shfl_sync(0xFFFFFFFFu, bias_l.z, src);
-        bv.w = __shfl_sync(0xFFFFFFFFu, bias_l.w, src);
-        return bv;
-      };
-      // A 32 x 32 bf16 chunk at columns n0, this lane's row in packed[0, 16).
-      // (With an activation, z and y may leave in different ways from the
-      // same buffers: every use of a buffer commits a group, an empty one
-      // where no TMA store was issued, so that "at most one group pending"
-      // always means that the buffer's last store has read it.)
-      auto store_bf16 = [&](int n0, const uint32_t(&packed)[16], const CUtensorMap* tm, uint16_t* base, bool tma) {
-        const uint32_t sbuf = stage0 + uint32_t(buf) * kStagingBytes;
-        // The buffer's previous TMA store has read it (checked after the math,
-        // so the wait overlaps it).
-        if ((tma || kAct) && lane == 0) bulk_wait_read_le1();
-        __syncwarp();
-        // 16-byte unit u of this lane's 64-byte row holds columns 8u .. 8u+7,
-        // at unit position u ^ ((lane >> 1) & 3).
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t addr = sbuf + uint32_t(lane) * 64u + uint32_t((u ^ ((lane >> 1) & 3)) * 16);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(packed[4 * u]),
-                       "r"(packed[4 * u + 1]), "r"(packed[4 * u + 2]), "r"(packed[4 * u + 3])
-                       : "memory");
-        }
-        if (tma) {
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(tm, sbuf, n0, m0, b);
-            bulk_commit();
-          }
-        } else {
-          // Rows not 16-byte aligned: the chunk staged in the same swizzled
-          // layout is written row by row, lane l taking column n0 + l, so
-          // each store instruction covers 64 contiguous bytes.
-          __syncwarp();
-          const bool col_ok = n0 + lane < p.N;
-          uint16_t* obase = base + int64_t(b) * p.c_stride + int64_t(m0) * p.N + n0 + lane;
-#pragma unroll 4
-          for (int rr = 0; rr < 32; ++rr) {
-            const uint32_t addr = sbuf + uint32_t(rr) * 64u + uint32_t((((lane >> 3) ^ ((rr >> 1) & 3)) << 4)) +
-                                  uint32_t((lane & 7) << 1);
-            uint16_t v16;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v16) : "r"(addr) : "memory");
-            if (col_ok && m0 + rr < p.M) obase[int64_t(rr) * p.N] = v16;
-          }
-          if (kAct && lane == 0) bulk_commit();
-        }
-        buf ^= 1;
-      };
-      // Activation epilogue of a chunk: v, accumulators in, becomes y.
-      auto act_chunk = [&](int n0, uint32_t(&v)[32]) {
-        uint32_t aux[16];
-        if (p.aux != nullptr) {
-          // Read row by row, lane l taking column n0 + l (64 contiguous bytes
-          // per load, any alignment), turned through a staging buffer.
-          const uint32_t sbuf = stage0 + uint32_t(buf) * kStagingBytes;
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
-          const bool col_ok = n0 + lane < p.N;
-          const uint16_t* abase = p.aux + int64_t(m0) * p.N + n0 + lane;
-#pragma unroll 16
-          for (int rr = 0; rr < 32; ++rr) {
-            const uint16_t a16 = col_ok && m0 + rr < p.M ? abase[int64_t(rr) * p.N] : uint16_t(0);
-            const uint32_t addr = sbuf + uint32_t(rr) * 64u + uint32_t((((lane >> 3) ^ ((rr >> 1) & 3)) << 4)) +
-                                  uint32_t((lane & 7) << 1);
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(a16) : "memory");
-          }
-          __syncwarp();
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint32_t addr = sbuf + uint32_t(lane) * 64u + uint32_t((u ^ ((lane >> 1) & 3)) * 16);
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(aux[4 * u]), "=r"(aux[4 * u + 1]), "=r"(aux[4 * u + 2]), "=r"(aux[4 * u + 3])
-                         : "r"(addr)
-                         : "memory");
-          }
-          __syncwarp();
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (has_bias) bv = bias_of(n0, j);
-          float* y = reinterpret_cast<float*>(v + 4 * j);
-          fma2(y[0], y[1], sab, bv.x, bv.y);
-          fma2(y[2], y[3], sab, bv.z, bv.w);
-        }
-        float* y = reinterpret_cast<float*>(v);
-        if (p.z != nullptr) {
-          uint32_t zp[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
-            zp[j] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          store_bf16(n0, zp, tmZ, p.z, p.z_tma != 0);
-        }
-        switch (p.act) {  // warp-uniform
-          case FP8_ACT_RELU:
-#pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] = act_value(FP8_ACT_RELU, y[j]);
-            break;
-          case FP8_ACT_GELU:
-#pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] = act_value(FP8_ACT_GELU, y[j]);
-            break;
-          case FP8_ACT_SILU:
-#pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] = act_value(FP8_ACT_SILU, y[j]);
-            break;
-          default: break;
-        }
-        if (p.aux != nullptr) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float lo = __uint_as_float(aux[j] << 16), hi = __uint_as_float(aux[j] & 0xFFFF0000u);
-            y[2 * j] = p.aux_mul ? __fmul_rn(y[2 * j], lo) : __fadd_rn(y[2 * j], lo);
-            y[2 * j + 1] = p.aux_mul ? __fmul_rn(y[2 * j + 1], hi) : __fadd_rn(y[2 * j + 1], hi);
-          }
-        }
-      };
       // One 32 x 32 chunk at output columns n0 (this lane's row): scale, bias,
       // one bf16 rounding, store.
-      auto emit = [&](int n0, uint32_t(&v)[32]) {
+      auto emit = [&](int n0, const uint32_t(&v)[32]) {
         if (m0 >= p.M) return;  // warp-uniform: rows beyond M (pair peer of a short last tile)
-        if constexpr (kAct) act_chunk(n0, v);
         const bool full = n0 + 32 <= p.N;
         const bool row_ok = m0 + lane < p.M;
         uint32_t packed[16];  // bf16 pairs, or (FP8 output) code quads in [0, 8)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (!kAct && has_bias) bv = bias_of(n0, j);
+          if (has_bias) {  // warp-uniform
+            const int src = ((n0 - nbase) >> 5) * 8 + j;
+            bv.x = __shfl_sync(0xFFFFFFFFu, bias_l.x, src);
+            bv.y = __shfl_sync(0xFFFFFFFFu, bias_l.y, src);
+            bv.z = __shfl_sync(0xFFFFFFFFu, bias_l.z, src);
+            bv.w = __shfl_sync(0xFFFFFFFFu, bias_l.w, src);
+          }
           float y0 = __uint_as_float(v[4 * j + 0]), y1 = __uint_as_float(v[4 * j + 1]);
           float y2 = __uint_as_float(v[4 * j + 2]), y3 = __uint_as_float(v[4 * j + 3]);
-          if constexpr (!kAct) {
-            fma2(y0, y1, sab, bv.x, bv.y);  // acc * sinv_a*sinv_b + bias, one rounding each
-            fma2(y2, y3, sab, bv.z, bv.w);
-          }
+          fma2(y0, y1, sab, bv.x, bv.y);  // acc * sinv_a*sinv_b + bias, one rounding each
+          fma2(y2, y3, sab, bv.z, bv.w);
           if constexpr (kOut8) {
             // amax over this lane's in-range elements (NaN ignored), then the
             // codes of y * s_out.
@@ -944,7 +1127,6 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
           // layout, then written row by row, lane l taking column n0 + l, so
           // each store instruction covers 32 contiguous bytes of one row.
           const uint32_t sbuf = stage0 + uint32_t(buf) * kStagingBytes;
-          if (kAct && lane == 0) bulk_wait_read_le1();
           __syncwarp();  // every lane has read this buffer's previous chunk
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -964,11 +1146,47 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
             asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v16) : "r"(addr) : "memory");
             if (col_ok && m0 + rr < p.M) obase[int64_t(rr) * p.N] = uint8_t(v16);
           }
-          if (kAct && lane == 0) bulk_commit();
           buf ^= 1;
           return;
         }
-        store_bf16(n0, packed, tmC, p.out, p.tma_store);
+        const uint32_t sbuf = stage0 + uint32_t(buf) * kStagingBytes;
+        // The buffer's previous TMA store has read it (checked after the math,
+        // so the wait overlaps it).
+        if (p.tma_store && lane == 0) bulk_wait_read_le1();
+        __syncwarp();
+        // 16-byte unit u of this lane's 64-byte row holds columns 8u .. 8u+7,
+        // at unit position u ^ ((lane >> 1) & 3).
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t addr = sbuf + uint32_t(lane) * 64u + uint32_t((u ^ ((lane >> 1) & 3)) * 16);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(packed[4 * u]),
+                       "r"(packed[4 * u + 1]), "r"(packed[4 * u + 2]), "r"(packed[4 * u + 3])
+                       : "memory");
+        }
+        if (p.tma_store) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(tmC, sbuf, n0, m0, b);
+            bulk_commit();
+          }
+        } else {
+          // Rows not 16-byte aligned: the chunk staged in the same swizzled
+          // layout is written row by row, lane l taking column n0 + l, so
+          // each store instruction covers 64 contiguous bytes.
+          __syncwarp();
+          const bool col_ok = n0 + lane < p.N;
+          uint16_t* obase = p.out + int64_t(b) * p.c_stride + int64_t(m0) * p.N + n0 + lane;
+#pragma unroll 4
+          for (int rr = 0; rr < 32; ++rr) {
+            const uint32_t addr = sbuf + uint32_t(rr) * 64u + uint32_t((((lane >> 3) ^ ((rr >> 1) & 3)) << 4)) +
+                                  uint32_t((lane & 7) << 1);
+            uint16_t v16;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v16) : "r"(addr) : "memory");
+            if (col_ok && m0 + rr < p.M) obase[int64_t(rr) * p.N] = v16;
+          }
+        }
+        buf ^= 1;
       };
       auto add4 = [](uint32_t* v, const float4& w) {
         v[0] = __float_as_uint(__uint_as_float(v[0]) + w.x);
@@ -1054,7 +1272,7 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
     }
     // The staging buffers are released once the stores have read them; waiting
     // for the global writes too kept every CTA alive ~0.4 us longer.
-    if ((p.tma_store || kAct) && lane == 0) bulk_wait_read_all();
+    if (p.tma_store && lane == 0) bulk_wait_read_all();
     __syncwarp();
   }
 
@@ -1082,16 +1300,16 @@ template <int BN, int PAIR, int EPI>
 __global__ void __launch_bounds__(kThreadsMM, 1)
     mm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ MmParams p) {
-  mm_body<BN, PAIR, EPI>(&tmA, &tmB, &tmC, nullptr, p, int(blockIdx.x) / PAIR, int(gridDim.x) / PAIR);
+  mm_body<BN, PAIR, EPI>(&tmA, &tmB, &tmC, p, int(blockIdx.x) / PAIR, int(gridDim.x) / PAIR);
 }
 
 // The product with an activation epilogue.
 template <int BN, int PAIR, int EPI>
 __global__ void __launch_bounds__(kThreadsMM, 1)
     mm_act_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                  const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmZ,
-                  const __grid_constant__ MmParams p) {
-  mm_body<BN, PAIR, EPI | kEpiAct>(&tmA, &tmB, &tmC, &tmZ, p, int(blockIdx.x) / PAIR, int(gridDim.x) / PAIR);
+                  const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmX,
+                  const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ MmParams p) {
+  mm_body<BN, PAIR, EPI | kEpiAct>(&tmA, &tmB, &tmC, p, int(blockIdx.x) / PAIR, int(gridDim.x) / PAIR, &tmX, &tmZ);
 }
 
 // Two independent GEMMs in one persistent launch (the dX and dW GEMMs of a
@@ -1105,8 +1323,8 @@ __global__ void __launch_bounds__(kThreadsMM, 1)
                        const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
                        const __grid_constant__ CUtensorMap tmC1, const __grid_constant__ MmParams p1, const int split) {
   const int g = int(blockIdx.x) / PAIR;
-  if (g < split) mm_body<BN, PAIR, 0>(&tmA0, &tmB0, &tmC0, nullptr, p0, g, split);
-  else mm_body<BN, PAIR, 0>(&tmA1, &tmB1, &tmC1, nullptr, p1, g - split, int(gridDim.x) / PAIR - split);
+  if (g < split) mm_body<BN, PAIR, 0>(&tmA0, &tmB0, &tmC0, p0, g, split);
+  else mm_body<BN, PAIR, 0>(&tmA1, &tmB1, &tmC1, p1, g - split, int(gridDim.x) / PAIR - split);
 }
 
 // K == 0: Y = bf16(bias) or 0.
@@ -1393,23 +1611,25 @@ int launch_mm(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t 
 
 template <int BN, int PAIR, int EPI>
 int launch_act_epi(const MmProblem& q, const MmChoice& c, cudaStream_t st) {
-  CUtensorMap ta, tb, tc, tz;
+  CUtensorMap ta, tb, tc, tx, tz;
   MmParams p = q.p;
   const int rc = prepare_mm<BN, PAIR>(q.A, q.B, q.M, q.N, q.K, 1, nullptr, p, c, nullptr, ta, tb, tc);
   if (rc != FP8_OK) return rc;
+  memset(&tx, 0, sizeof(tx));
   memset(&tz, 0, sizeof(tz));
+  if (p.aux_tma && !make_out_map(&tx, const_cast<uint16_t*>(p.aux), q.M, q.N, 1, q.M * q.N)) return FP8_ERR_CUDA;
   if (p.z_tma && !make_out_map(&tz, p.z, q.M, q.N, 1, q.M * q.N)) return FP8_ERR_CUDA;
   static bool done[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8_ERR_CUDA;
   if (!done[dev]) {
     if (cudaFuncSetAttribute(mm_act_kernel<BN, PAIR, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg<BN, PAIR>::kSmemBytes) != cudaSuccess)
+                             ActCfg<BN, PAIR>::kSmemBytes) != cudaSuccess)
       return FP8_ERR_CUDA;
     done[dev] = true;
   }
   const cudaError_t e = launch_pdl(mm_act_kernel<BN, PAIR, EPI>, dim3(PAIR * std::max(1, c.grid)), dim3(kThreadsMM),
-                                   Cfg<BN, PAIR>::kSmemBytes, st, PAIR, ta, tb, tc, tz, p);
+                                   ActCfg<BN, PAIR>::kSmemBytes, st, PAIR, ta, tb, tc, tx, tz, p);
   return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
@@ -1799,6 +2019,7 @@ extern "C" int fp8_mm_act(const fp8_mm_act_args* a, fp8_stream_t stream) {
   p.a_rows = a->sinv_a_rows != 0;
   p.aux = a->aux;
   p.aux_mul = a->aux_op == FP8_AUX_MUL;
+  p.aux_tma = a->aux != nullptr && on(a->aux, 16) && a->N % 8 == 0;
   p.z = a->z;
   p.z_tma = a->z != nullptr && on(a->z, 16) && a->N % 8 == 0;
   if (q.K == 0)
