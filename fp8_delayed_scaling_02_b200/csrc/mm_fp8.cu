@@ -60,6 +60,8 @@ constexpr int kStagingBytes = 2048;  // one 32x32 bf16 box per staging buffer
 // holds 128 rows of A, BN/2 rows of B and its 128 x BN half of the accumulator.
 template <int BN, int PAIR>
 struct Cfg {
+  static constexpr int kWarps = kEpiWarps;
+  static constexpr int kStallBar = 2 * ((192 * 1024) / (kBM * kBK + BN / PAIR * kBK)) + 11;  // after 8 amax slots
   static constexpr int kBRows = BN / PAIR;
   static constexpr int kABytes = kBM * kBK;
   static constexpr int kBBytes = kBRows * kBK;
@@ -74,20 +76,24 @@ struct Cfg {
                 "barrier area: barriers, TMEM slot, abort, amax, stall barrier");
 };
 
-// The same with an activation epilogue, whose warps each have four buffers for
-// the operand that turns into the output in place (two loads ahead, one in
-// work, one leaving) and two for the kept pre-activation: four stages are left
-// of six on CTA pairs, which still cover a load's way from L2.
-constexpr int kActBufs = 4, kActZBufs = 2;
+// The same with an activation epilogue: sixteen warps share it (eight for 64
+// columns), each with three staging buffers.  Four stages are left of six on
+// CTA pairs, which still cover a load's way from L2.
+constexpr int kActBufs = 3;
 template <int BN, int PAIR>
 struct ActCfg : Cfg<BN, PAIR> {
   using B = Cfg<BN, PAIR>;
-  static constexpr int kWarpStaging = (kActBufs + kActZBufs) * kStagingBytes;
-  static constexpr int kStages = (232448 - 512 - 1024 - kEpiWarps * kWarpStaging) / B::kStageBytes;
+  static constexpr int kWarps = BN >= 128 ? 16 : 8;
+  static constexpr int kThreads = 32 * (2 + kWarps);
+  static constexpr int kWarpCols = BN * 4 / kWarps;  // four TMEM lane quadrants
+  static constexpr int kWarpStaging = kActBufs * kStagingBytes;
+  static constexpr int kStages = (232448 - 768 - 1024 - kWarps * kWarpStaging) / B::kStageBytes;
   static constexpr int kStagingOffset = kStages * B::kStageBytes;
-  static constexpr int kBarOffset = kStagingOffset + kEpiWarps * kWarpStaging;
-  static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
+  static constexpr int kBarOffset = kStagingOffset + kWarps * kWarpStaging;
+  static constexpr int kSmemBytes = kBarOffset + 768 + 1024;
+  static constexpr int kStallBar = 2 * kStages + 15;  // after 16 amax slots
   static_assert(kSmemBytes <= 232448 && kStages >= 2, "shared memory budget");
+  static_assert(kStallBar * 8 + 8 <= 256 && 256 + 8 * kActBufs * kWarps <= 768, "barrier area");
 };
 
 struct MmParams {
@@ -168,10 +174,11 @@ __device__ __forceinline__ float4 bias8_4(const MmParams& p, int n, float bsc) {
 // the grid's amax, clears the scratch words and commits the ring.  ring_s
 // holds the ring's history, idx and scale as read at launch (only this fold
 // writes them).  Run by one thread after the CTA's epilogue.
+template <int kWarps>
 __device__ __noinline__ void out8_ticket_fold(const MmParams& p, const float* amax_s, const float* ring_s) {
   float m = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kEpiWarps; ++w) m = fmaxf(m, amax_s[w]);
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, amax_s[w]);
   // The CTA's amax goes in with an atom.max whose return value the ticket's
   // address depends on (bit 31 of a non-negative float: 0 at run time,
   // opaque to the compiler), so the ticket is issued only once the amax is
@@ -477,13 +484,19 @@ __device__ __forceinline__ void decode_tile(const MmParams& p, int t, int& b, in
 
 // ---- activation epilogue -----------------------------------------------------------
 //
-// y = act(z) [+ or * aux] for z = acc * sinv + bias, by the eight epilogue
-// warps of a CTA, each a 32-row quadrant by half the tile's columns in chunks
-// of 32 x 32.  Per chunk: TMEM -> z; z in bf16 to a z buffer; act; the aux
-// chunk, which a TMA load has put into the chunk's buffer; the result over it
-// in place; one group of TMA stores for z and y.  The load for the chunk after
-// next is issued as each chunk begins, across tiles, into the buffer whose
-// store is two groups back, so neither its latency nor a store's is waited for.
+// y = act(z) [+ or * aux] for z = acc * sinv + bias, each warp a 32-row
+// quadrant by its share of the tile's columns in chunks of 32 x 32.  Per
+// chunk: TMEM -> z; z in bf16 to a free buffer; act; the aux chunk, which a TMA
+// load has put into the chunk's buffer; the result over it in place; one group
+// of TMA stores for z and y.  The next chunk's load, in the next tile where
+// need be, is issued as a chunk begins.  A chunk is a chain of about 2 us
+// (TMEM, shared memory, MUFU, fences), so it takes four warps per scheduler to
+// keep the issue slots busy: eight warps of two 8192x4096 tiles ran 40% full
+// and 54 us of epilogue alone (K = 128).
+// Buffers: chunk q works in slot G q mod 3 and keeps z in the next, G = 2 with
+// z and 1 without.  A slot is written again only after the group of the chunk
+// that used it last has read it: the previous chunk with z, else the one
+// before that.
 // Tensors whose rows are not 16-byte multiples go through the same buffers by
 // guarded accesses, 64 contiguous bytes of one row per warp access.
 
@@ -492,16 +505,17 @@ struct ActTile {
 };
 
 template <int BN, int PAIR>
-__device__ __forceinline__ bool act_tile(const MmParams& p, int cta, int ctas, uint32_t rank, int quad, int half, int i,
+__device__ __forceinline__ bool act_tile(const MmParams& p, int cta, int ctas, uint32_t rank, int quad, int part, int i,
                                          ActTile& t) {
+  constexpr int kCols = ActCfg<BN, PAIR>::kWarpCols;
   const int tile = cta + i * ctas;
   if (tile >= p.dp_tiles) return false;
   int b, mt, nt;
   decode_tile(p, tile, b, mt, nt);
   t.i = i;
   t.m0 = mt * kBM * PAIR + int(rank) * kBM + quad * 32;
-  t.nbase = nt * BN + half * (BN / 2);
-  t.chunks = t.m0 >= p.M || t.nbase >= p.N ? 0 : min(BN / 64, (p.N - t.nbase + 31) / 32);
+  t.nbase = nt * BN + part * kCols;
+  t.chunks = t.m0 >= p.M || t.nbase >= p.N ? 0 : min(kCols / 32, (p.N - t.nbase + 31) / 32);
   return true;
 }
 
@@ -523,43 +537,47 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
                                               const int ew, const int quad, const int lane, const uint32_t staging,
                                               const uint32_t tmem_base, const uint32_t bar0, volatile int* abort) {
   using C = ActCfg<BN, PAIR>;
-  const int half = ew >> 2;
+  const int part = ew >> 2;
   const uint32_t tfull0 = bar0 + 8u * (2 * C::kStages), tempty0 = tfull0 + 16u;
-  const uint32_t stall_bar = bar0 + 8u * (2 * C::kStages + 11);
+  const uint32_t stall_bar = bar0 + 8u * C::kStallBar;
   const uint32_t aux_bar = bar0 + 256u + 8u * (kActBufs * ew);
-  const uint32_t bufs = staging + uint32_t(ew) * C::kWarpStaging, zbufs = bufs + kActBufs * kStagingBytes;
+  const uint32_t bufs = staging + uint32_t(ew) * C::kWarpStaging;
   const float sinv_b = *p.sinv_b;
   const float sab_all = __fmul_rn(*p.sinv_a, sinv_b);
   const float s_out = kOut8 ? *p.r_scale : 0.0f;
   const bool prefetch = p.aux != nullptr && p.aux_tma;
   float amax = 0.0f;
 
-  // The next aux chunk to ask for: chunk `pc` of tile `pt`, number `pq` in this warp's sequence.
+  auto next_slot = [&](uint32_t s) {  // the slot of the chunk after the one in slot s
+    s += p.z != nullptr ? 2u : 1u;
+    return s >= kActBufs ? s - kActBufs : s;
+  };
+  // The next aux chunk to ask for: chunk `pc` of tile `pt`, into `pslot`.
   ActTile pt{-1, 0, 0, 0};
   int pc = 0;
-  uint32_t pq = 0;
+  uint32_t pslot = 0;
   bool more = prefetch;
   auto ask = [&]() {  // warp-uniform; lane 0 issues
     while (more && pc >= pt.chunks) {
       pc = 0;
-      more = act_tile<BN, PAIR>(p, cta, ctas, rank, quad, half, pt.i + 1, pt);
+      more = act_tile<BN, PAIR>(p, cta, ctas, rank, quad, part, pt.i + 1, pt);
     }
     if (!more) return;
     if (lane == 0) {
-      const uint32_t b = pq & (kActBufs - 1);
-      mbar_arrive_expect_tx(aux_bar + 8u * b, kStagingBytes);
-      tma_load_3d(bufs + b * kStagingBytes, tmX, pt.nbase + 32 * pc, pt.m0, 0, aux_bar + 8u * b);
+      mbar_arrive_expect_tx(aux_bar + 8u * pslot, kStagingBytes);
+      tma_load_3d(bufs + pslot * kStagingBytes, tmX, pt.nbase + 32 * pc, pt.m0, 0, aux_bar + 8u * pslot);
     }
     ++pc;
-    ++pq;
+    pslot = next_slot(pslot);
   };
   ask();
-  ask();
 
-  uint32_t q = 0;  // chunks done
+  // Slot of the chunk in work; parity of its slot's next load, which flips
+  // each time all three have had their turn.
+  uint32_t slot = 0, parity = 0, turn = 0;
   bool ok = true;
   ActTile t;
-  for (int i = 0; ok && act_tile<BN, PAIR>(p, cta, ctas, rank, quad, half, i, t); ++i) {
+  for (int i = 0; ok && act_tile<BN, PAIR>(p, cta, ctas, rank, quad, part, i, t); ++i) {
     const int acc = i & 1;
     // (Testing: with the stall site set here, the wait is on a barrier that
     // nothing completes, so it runs out and the abort path runs.)
@@ -578,14 +596,14 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
       release();
       continue;
     }
-    const uint32_t tbase = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * (BN / 2));
+    const uint32_t tbase = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + part * C::kWarpCols);
     const int m = t.m0 + lane;
     const bool row_ok = m < p.M;
     float sab = sab_all;
     if (p.a_rows) sab = row_ok ? __fmul_rn(__ldg(p.sinv_a + m), sinv_b) : 0.0f;
     // Bias of columns nbase + 4 lane .. + 3, read once per tile, handed out by shuffle.
     float4 bias_l = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.bias != nullptr && lane < BN / 8) {
+    if (p.bias != nullptr && lane < C::kWarpCols / 4) {
       const int c4 = t.nbase + 4 * lane;
       bias_l.x = c4 < p.N ? __ldg(p.bias + c4) : 0.f;
       bias_l.y = c4 + 1 < p.N ? __ldg(p.bias + c4 + 1) : 0.f;
@@ -593,25 +611,23 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
       bias_l.w = c4 + 3 < p.N ? __ldg(p.bias + c4 + 3) : 0.f;
     }
 #pragma unroll 1
-    for (int c = 0; c < t.chunks; ++c, ++q) {
+    for (int c = 0; c < t.chunks; ++c) {
       const int n0 = t.nbase + 32 * c;
-      const uint32_t buf = bufs + (q & (kActBufs - 1)) * kStagingBytes;
-      const uint32_t zbuf = zbufs + (q & (kActZBufs - 1)) * kStagingBytes;
+      const uint32_t buf = bufs + slot * kStagingBytes;
+      const uint32_t zbuf = bufs + (slot == kActBufs - 1 ? 0u : slot + 1u) * kStagingBytes;
       uint32_t r[32];
       __syncwarp();
       tmem_ld32_nowait(tbase + uint32_t(32 * c), r);
-      // One group per chunk: with at most one pending, the stores of the chunk
-      // two back have read their buffers, which the next load and z reuse.
-      if (lane == 0) bulk_wait_read_le1();
+      if (lane == 0) {  // one group per chunk
+        if (p.z != nullptr) bulk_wait_read_all();
+        else bulk_wait_read_le1();
+      }
       __syncwarp();
       ask();
       uint32_t aux[16];
       if (p.aux != nullptr) {
         if (p.aux_tma) {
-          if (!mbar_wait(aux_bar + 8u * (q & (kActBufs - 1)), (q / kActBufs) & 1, abort, p.err, kWaitEpilogueAux,
-                         p.wait_ns)) {
-            ok = false;
-          }
+          ok = mbar_wait(aux_bar + 8u * slot, parity, abort, p.err, kWaitEpilogueAux, p.wait_ns);
           ok = __all_sync(0xFFFFFFFFu, ok);
         } else {
           const bool col_ok = n0 + lane < p.N;
@@ -734,15 +750,23 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
         if (p.tma_store) tma_store_3d(tmC, buf, n0, t.m0, 0);
         bulk_commit();
       }
+      slot = next_slot(slot);
+      if (++turn == kActBufs) {
+        turn = 0;
+        parity ^= 1u;
+      }
     }
   }
   if (lane == 0) {
-    // Loads asked for and not consumed (only after a wait gave up) land before
-    // shared memory is released; stores have read it.
-    for (; q < pq; ++q) {
+    // Loads asked for and not consumed (only after a wait gave up, at most two)
+    // land before shared memory is released; stores have read it.
+    for (; prefetch && slot != pslot; slot = next_slot(slot)) {
       const unsigned long long t0 = globaltimer_ns();
-      while (!mbar_try_wait(aux_bar + 8u * (q & (kActBufs - 1)), (q / kActBufs) & 1) &&
-             globaltimer_ns() - t0 < kWaitBudgetNs) {
+      while (!mbar_try_wait(aux_bar + 8u * slot, parity) && globaltimer_ns() - t0 < kWaitBudgetNs) {
+      }
+      if (++turn == kActBufs) {
+        turn = 0;
+        parity ^= 1u;
       }
     }
     bulk_wait_read_all();
@@ -759,6 +783,7 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
                                         const CUtensorMap* tmX = nullptr, const CUtensorMap* tmZ = nullptr) {
   constexpr bool kAct = (EPI & kEpiAct) != 0;
   using C = std::conditional_t<kAct, ActCfg<BN, PAIR>, Cfg<BN, PAIR>>;
+  constexpr int kEW = C::kWarps;  // epilogue warps
   constexpr bool kOut8 = (EPI & kEpiOut8) != 0;
   constexpr bool kBias8 = (EPI & kEpiBias8) != 0;
   constexpr int kTileM = kBM * PAIR;
@@ -779,7 +804,7 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * C::kStages + 2 + a); };
   const uint32_t done_bar = bar0 + 8u * (2 * C::kStages + 4);
   // After the TMEM slot, abort flag and amax slots: never arrived on.
-  const uint32_t stall_bar = bar0 + 8u * (2 * C::kStages + 11);
+  const uint32_t stall_bar = bar0 + 8u * C::kStallBar;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -794,12 +819,12 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), kEpiWarps * PAIR);
+      mbar_init(tempty_bar(a), kEW * PAIR);
     }
     mbar_init(done_bar, 1);
     mbar_init(stall_bar, 1);
     if constexpr (kAct) {
-      for (int k = 0; k < kActBufs * kEpiWarps; ++k) mbar_init(bar0 + 256u + 8u * k, 1);
+      for (int k = 0; k < kActBufs * kEW; ++k) mbar_init(bar0 + 256u + 8u * k, 1);
     }
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1285,7 +1310,7 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
       float* ring_s = reinterpret_cast<float*>(smem + C::kStagingOffset);
       if (lane <= kHistoryLen + 1) ring_s[lane] = ring_v;
       __syncwarp();
-      if (lane == 0) out8_ticket_fold(p, amax_s, ring_s);
+      if (lane == 0) out8_ticket_fold<kEW>(p, amax_s, ring_s);
       __syncwarp();
     }
   }
@@ -1305,7 +1330,7 @@ __global__ void __launch_bounds__(kThreadsMM, 1)
 
 // The product with an activation epilogue.
 template <int BN, int PAIR, int EPI>
-__global__ void __launch_bounds__(kThreadsMM, 1)
+__global__ void __launch_bounds__(ActCfg<BN, PAIR>::kThreads, 1)
     mm_act_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmX,
                   const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ MmParams p) {
@@ -1628,7 +1653,7 @@ int launch_act_epi(const MmProblem& q, const MmChoice& c, cudaStream_t st) {
       return FP8_ERR_CUDA;
     done[dev] = true;
   }
-  const cudaError_t e = launch_pdl(mm_act_kernel<BN, PAIR, EPI>, dim3(PAIR * std::max(1, c.grid)), dim3(kThreadsMM),
+  const cudaError_t e = launch_pdl(mm_act_kernel<BN, PAIR, EPI>, dim3(PAIR * std::max(1, c.grid)), dim3(ActCfg<BN, PAIR>::kThreads),
                                    ActCfg<BN, PAIR>::kSmemBytes, st, PAIR, ta, tb, tc, tx, tz, p);
   return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
