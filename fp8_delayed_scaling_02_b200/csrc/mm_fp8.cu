@@ -76,24 +76,28 @@ struct Cfg {
                 "barrier area: barriers, TMEM slot, abort, amax, stall barrier");
 };
 
-// The same with an activation epilogue: sixteen warps share it (eight for 64
-// columns), each with three staging buffers.  Four stages are left of six on
-// CTA pairs, which still cover a load's way from L2.
-constexpr int kActBufs = 3;
-template <int BN, int PAIR>
+// The same with an activation epilogue: one epilogue warp per 32 x 64 piece of
+// the CTA's tile, each with a 4 KB buffer for the operand that z or y replaces
+// in place and, where both z and an output leave, one for the other (codes: 2
+// KB).  On CTA pairs that leaves five stages (bf16 out), four (codes) or three
+// (bf16 out and z) of six; each covers a load's way from L2.
+constexpr int kEpiOut8 = 1;   // EPI bit: FP8 output codes + output ring fold
+constexpr int kEpiBias8 = 2;  // EPI bit: FP8 bias codes
+constexpr int kEpiAct = 4;    // EPI bit: activation, residual or gate operand, kept pre-activation
+constexpr int kEpiZ = 8;      // EPI bit, with kEpiAct and bf16 output: z is kept
+template <int BN, int PAIR, int EPI>
 struct ActCfg : Cfg<BN, PAIR> {
   using B = Cfg<BN, PAIR>;
-  static constexpr int kWarps = BN >= 128 ? 16 : 8;
+  static constexpr int kWarps = BN / 16;
   static constexpr int kThreads = 32 * (2 + kWarps);
-  static constexpr int kWarpCols = BN * 4 / kWarps;  // four TMEM lane quadrants
-  static constexpr int kWarpStaging = kActBufs * kStagingBytes;
-  static constexpr int kStages = (232448 - 768 - 1024 - kWarps * kWarpStaging) / B::kStageBytes;
+  static constexpr int kBufA = 4096, kBufB = EPI & kEpiOut8 ? 2048 : EPI & kEpiZ ? 4096 : 0;
+  static constexpr int kStages = (232448 - 512 - 1024 - kWarps * (kBufA + kBufB)) / B::kStageBytes;
   static constexpr int kStagingOffset = kStages * B::kStageBytes;
-  static constexpr int kBarOffset = kStagingOffset + kWarps * kWarpStaging;
-  static constexpr int kSmemBytes = kBarOffset + 768 + 1024;
+  static constexpr int kBarOffset = kStagingOffset + kWarps * (kBufA + kBufB);
+  static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
   static constexpr int kStallBar = 2 * kStages + 15;  // after 16 amax slots
   static_assert(kSmemBytes <= 232448 && kStages >= 2, "shared memory budget");
-  static_assert(kStallBar * 8 + 8 <= 256 && 256 + 8 * kActBufs * kWarps <= 768, "barrier area");
+  static_assert(kStallBar * 8 + 8 <= 256 && 256 + 8 * kWarps <= 512, "barrier area");
 };
 
 struct MmParams {
@@ -149,11 +153,8 @@ struct MmParams {
   int aux_tma;          // aux comes through TMA loads (tmX valid)
   uint16_t* z;          // bf16 [M, N], or null
   int z_tma;            // z leaves through TMA stores (tmZ valid)
+  float inv_span;       // 1 / (tiles of a full group of 8 m-tiles)
 };
-
-constexpr int kEpiOut8 = 1;   // EPI bit: FP8 output codes + output ring fold
-constexpr int kEpiBias8 = 2;  // EPI bit: FP8 bias codes
-constexpr int kEpiAct = 4;    // EPI bit: activation, residual or gate operand, kept pre-activation
 
 // Value of one FP8 code (exact in fp32; NaN codes give NaN).
 __device__ __forceinline__ float fp8_value(uint8_t c, int fmt) {
@@ -402,6 +403,25 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[3
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Waits for the load into r: no use of r moves ahead of it.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
 // Shared-memory matrix descriptor of a K-major tile written by TMA with the
 // 128-byte swizzle: 8-row x 128-byte atoms stacked along M/N every 1024 bytes
 // (stride byte offset), leading byte offset unused for this layout, version 1,
@@ -484,101 +504,176 @@ __device__ __forceinline__ void decode_tile(const MmParams& p, int t, int& b, in
 
 // ---- activation epilogue -----------------------------------------------------------
 //
-// y = act(z) [+ or * aux] for z = acc * sinv + bias, each warp a 32-row
-// quadrant by its share of the tile's columns in chunks of 32 x 32.  Per
-// chunk: TMEM -> z; z in bf16 to a free buffer; act; the aux chunk, which a TMA
-// load has put into the chunk's buffer; the result over it in place; one group
-// of TMA stores for z and y.  The next chunk's load, in the next tile where
-// need be, is issued as a chunk begins.  A chunk is a chain of about 2 us
-// (TMEM, shared memory, MUFU, fences), so it takes four warps per scheduler to
-// keep the issue slots busy: eight warps of two 8192x4096 tiles ran 40% full
-// and 54 us of epilogue alone (K = 128).
-// Buffers: chunk q works in slot G q mod 3 and keeps z in the next, G = 2 with
-// z and 1 without.  A slot is written again only after the group of the chunk
-// that used it last has read it: the previous chunk with z, else the one
-// before that.
+// y = act(z) [+ or * aux] for z = acc * sinv + bias.  Each epilogue warp has the
+// 32 x 64 piece of every tile at its TMEM lane quadrant and its quarter of the
+// columns (half, or all, of narrower tiles).  The aux piece is in the warp's
+// buffer before the tile's products are: a TMA load for the next tile goes out
+// as soon as this tile's stores have read the buffer.  Sixteen columns at a
+// time: TMEM -> z -> act -> y, written over the aux units just read (codes
+// beside them); then one group of TMA stores.
+// Rows of a box are 128 bytes: an SM's TMA unit takes a row of a box about
+// every four cycles however short it is, and 64-byte rows (32 columns a box)
+// made the epilogue of an 8192 x 4096 output 46 us long by itself (K = 128,
+// gated, z kept), more than the products of K = 1536.
 // Tensors whose rows are not 16-byte multiples go through the same buffers by
-// guarded accesses, 64 contiguous bytes of one row per warp access.
+// guarded accesses of one row at a time.
 
-struct ActTile {
-  int i, chunks, m0, nbase;  // tile ordinal of this CTA, valid chunks, first row and column of this warp
+struct ActPiece {
+  int i, m0, n0;  // tile ordinal of this CTA; first row and column of this warp's piece
+  bool any;       // part of the output
 };
 
 template <int BN, int PAIR>
-__device__ __forceinline__ bool act_tile(const MmParams& p, int cta, int ctas, uint32_t rank, int quad, int part, int i,
-                                         ActTile& t) {
-  constexpr int kCols = ActCfg<BN, PAIR>::kWarpCols;
+__device__ __forceinline__ bool act_piece(const MmParams& p, int cta, int ctas, uint32_t rank, int quad, int part, int i,
+                                          ActPiece& t) {
   const int tile = cta + i * ctas;
   if (tile >= p.dp_tiles) return false;
-  int b, mt, nt;
-  decode_tile(p, tile, b, mt, nt);
+  // decode_tile's order for one batch of groups of 8 m-tiles.  The division by
+  // a group's tiles is a product with its inverse, at most one off (there are
+  // fewer than 2^20 groups), that by its rows a shift but in a short last group.
+  const int span = 8 * p.n_tiles;
+  int g = int(float(tile) * p.inv_span);
+  int rr = tile - g * span;
+  if (rr < 0) {
+    --g;
+    rr += span;
+  } else if (rr >= span) {
+    ++g;
+    rr -= span;
+  }
+  const int gm = p.m_tiles - 8 * g;
+  const int nt = gm >= 8 ? rr >> 3 : rr / gm;
+  const int mt = 8 * g + (gm >= 8 ? rr & 7 : rr - nt * gm);
   t.i = i;
   t.m0 = mt * kBM * PAIR + int(rank) * kBM + quad * 32;
-  t.nbase = nt * BN + part * kCols;
-  t.chunks = t.m0 >= p.M || t.nbase >= p.N ? 0 : min(kCols / 32, (p.N - t.nbase + 31) / 32);
+  t.n0 = nt * BN + part * 64;
+  t.any = t.m0 < p.M && t.n0 < p.N;
   return true;
 }
 
-// act(y) of a chunk, two elements at a time.
+// act of sixteen values, two at a time.
 template <int ACT>
-__device__ __forceinline__ void act_chunk(float (&y)[32]) {
+__device__ __forceinline__ void act16(float (&y)[16]) {
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) act_pair<ACT>(y[j], y[j + 1]);
+  for (int j = 0; j < 16; j += 2) act_pair<ACT>(y[j], y[j + 1]);
 }
 
-// 16-byte unit u of row r of a 32 x 32 bf16 buffer (TMA's 64-byte swizzle).
+// 16-byte unit u of row r of a 32 x 64 bf16 buffer (TMA's 128-byte swizzle)
+// and of a 32 x 64 code buffer (64-byte swizzle).
+__device__ __forceinline__ uint32_t unit128(uint32_t buf, int r, int u) {
+  return buf + uint32_t(r) * 128u + uint32_t((u ^ (r & 7)) * 16);
+}
 __device__ __forceinline__ uint32_t unit64(uint32_t buf, int r, int u) {
   return buf + uint32_t(r) * 64u + uint32_t((u ^ ((r >> 1) & 3)) * 16);
 }
+__device__ __forceinline__ uint32_t bf16_at(uint32_t buf, int r, int c) { return unit128(buf, r, c >> 3) + 2u * (c & 7); }
 
-template <int BN, int PAIR, bool kOut8>
+// Rows that TMA cannot write: lane l takes columns n0 + l and n0 + 32 + l of
+// each row, 64 contiguous bytes a warp access.
+__device__ __forceinline__ void store_rows_bf16(const MmParams& p, uint16_t* base, uint32_t buf, const ActPiece& t,
+                                                int lane) {
+  for (int k = 0; k < 2; ++k) {
+    const int col = 32 * k + lane;
+    if (t.n0 + col >= p.N) break;
+    uint16_t* o = base + int64_t(t.m0) * p.N + t.n0 + col;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      uint16_t v;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(bf16_at(buf, r, col)) : "memory");
+      if (t.m0 + r < p.M) o[int64_t(r) * p.N] = v;
+    }
+  }
+}
+__device__ __forceinline__ void store_rows_codes(const MmParams& p, uint32_t buf, const ActPiece& t, int lane) {
+  for (int k = 0; k < 2; ++k) {
+    const int col = 32 * k + lane;
+    if (t.n0 + col >= p.N) break;
+    uint8_t* o = p.out8 + int64_t(t.m0) * p.N + t.n0 + col;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      uint16_t v;
+      asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(unit64(buf, r, col >> 4) + uint32_t(col & 15)) : "memory");
+      if (t.m0 + r < p.M) o[int64_t(r) * p.N] = uint8_t(v);
+    }
+  }
+}
+__device__ __forceinline__ void load_rows_bf16(const MmParams& p, uint32_t buf, const ActPiece& t, int lane) {
+  for (int k = 0; k < 2; ++k) {
+    const int col = 32 * k + lane;
+    const bool col_ok = t.n0 + col < p.N;
+    const uint16_t* src = p.aux + int64_t(t.m0) * p.N + t.n0 + col;
+#pragma unroll 16
+    for (int r = 0; r < 32; ++r) {
+      const uint16_t v = col_ok && t.m0 + r < p.M ? src[int64_t(r) * p.N] : uint16_t(0);
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(bf16_at(buf, r, col)), "h"(v) : "memory");
+    }
+  }
+}
+
+template <int BN, int PAIR, int EPI>
 __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUtensorMap* tmX, const CUtensorMap* tmZ,
                                               const MmParams& p, const int cta, const int ctas, const uint32_t rank,
                                               const int ew, const int quad, const int lane, const uint32_t staging,
                                               const uint32_t tmem_base, const uint32_t bar0, volatile int* abort) {
-  using C = ActCfg<BN, PAIR>;
+  using C = ActCfg<BN, PAIR, EPI>;
+  constexpr bool kOut8 = (EPI & kEpiOut8) != 0;
   const int part = ew >> 2;
   const uint32_t tfull0 = bar0 + 8u * (2 * C::kStages), tempty0 = tfull0 + 16u;
   const uint32_t stall_bar = bar0 + 8u * C::kStallBar;
-  const uint32_t aux_bar = bar0 + 256u + 8u * (kActBufs * ew);
-  const uint32_t bufs = staging + uint32_t(ew) * C::kWarpStaging;
+  const uint32_t aux_bar = bar0 + 256u + 8u * ew;
+  const uint32_t bufa = staging + uint32_t(ew) * C::kBufA;
+  const uint32_t bufb = staging + uint32_t(C::kWarps) * C::kBufA + uint32_t(ew) * C::kBufB;
+  const bool has_z = kOut8 ? p.z != nullptr : (EPI & kEpiZ) != 0;
+  // z lies over the aux units when codes leave, beside them when y does.
+  const uint32_t zbuf = kOut8 ? bufa : bufb;
   const float sinv_b = *p.sinv_b;
   const float sab_all = __fmul_rn(*p.sinv_a, sinv_b);
   const float s_out = kOut8 ? *p.r_scale : 0.0f;
-  const bool prefetch = p.aux != nullptr && p.aux_tma;
+  const bool has_aux = p.aux != nullptr;
+  const bool prefetch = has_aux && p.aux_tma;
   float amax = 0.0f;
 
-  auto next_slot = [&](uint32_t s) {  // the slot of the chunk after the one in slot s
-    s += p.z != nullptr ? 2u : 1u;
-    return s >= kActBufs ? s - kActBufs : s;
-  };
-  // The next aux chunk to ask for: chunk `pc` of tile `pt`, into `pslot`.
-  ActTile pt{-1, 0, 0, 0};
-  int pc = 0;
-  uint32_t pslot = 0;
-  bool more = prefetch;
+  // The piece whose aux has been asked for, or is to be next.
+  ActPiece nx{-1, 0, 0, false};
+  bool asked = false;
   auto ask = [&]() {  // warp-uniform; lane 0 issues
-    while (more && pc >= pt.chunks) {
-      pc = 0;
-      more = act_tile<BN, PAIR>(p, cta, ctas, rank, quad, part, pt.i + 1, pt);
-    }
-    if (!more) return;
+    asked = false;
+    do {
+      if (!act_piece<BN, PAIR>(p, cta, ctas, rank, quad, part, nx.i + 1, nx)) return;
+    } while (!nx.any);
+    asked = true;
     if (lane == 0) {
-      mbar_arrive_expect_tx(aux_bar + 8u * pslot, kStagingBytes);
-      tma_load_3d(bufs + pslot * kStagingBytes, tmX, pt.nbase + 32 * pc, pt.m0, 0, aux_bar + 8u * pslot);
+      mbar_arrive_expect_tx(aux_bar, C::kBufA);
+      tma_load_3d(bufa, tmX, nx.n0, nx.m0, 0, aux_bar);
     }
-    ++pc;
-    pslot = next_slot(pslot);
   };
-  ask();
-
-  // Slot of the chunk in work; parity of its slot's next load, which flips
-  // each time all three have had their turn.
-  uint32_t slot = 0, parity = 0, turn = 0;
-  bool ok = true;
-  ActTile t;
-  for (int i = 0; ok && act_tile<BN, PAIR>(p, cta, ctas, rank, quad, part, i, t); ++i) {
+  if (prefetch) ask();
+  uint32_t aux_par = 0;
+  ActPiece t;
+  for (int i = 0; act_piece<BN, PAIR>(p, cta, ctas, rank, quad, part, i, t); ++i) {
     const int acc = i & 1;
+    const int cols = t.any ? min(64, p.N - t.n0) : 0;
+    const int m = t.m0 + lane;
+    const bool row_ok = m < p.M;
+    float sab = sab_all;
+    if (p.a_rows) sab = row_ok ? __fmul_rn(__ldg(p.sinv_a + m), sinv_b) : 0.0f;
+    float2 bias_l = make_float2(0.f, 0.f);  // columns n0 + 2 lane, + 1: handed out by shuffle
+    if (p.bias != nullptr && 2 * lane < cols) {
+      bias_l.x = __ldg(p.bias + t.n0 + 2 * lane);
+      if (2 * lane + 1 < cols) bias_l.y = __ldg(p.bias + t.n0 + 2 * lane + 1);
+    }
+    if (has_aux && t.any) {
+      if (prefetch) {
+        bool ok = mbar_wait(aux_bar, aux_par, abort, p.err, kWaitEpilogueAux, p.wait_ns);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        asked = false;
+        aux_par ^= 1u;
+      } else {
+        load_rows_bf16(p, bufa, t, lane);
+        __syncwarp();
+      }
+    }
     // (Testing: with the stall site set here, the wait is on a barrier that
     // nothing completes, so it runs out and the abort path runs.)
     const bool stall = p.stall == kWaitEpilogueTmemFull;
@@ -586,190 +681,109 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
                    kWaitEpilogueTmemFull, p.wait_ns))
       break;
     tc_fence_after();
-    const uint32_t release_bar = PAIR == 1 ? tempty0 + 8u * acc : mapa_shared(tempty0 + 8u * acc, 0);
-    auto release = [&]() {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(release_bar);
-    };
-    if (t.chunks == 0) {
-      release();
-      continue;
-    }
-    const uint32_t tbase = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + part * C::kWarpCols);
-    const int m = t.m0 + lane;
-    const bool row_ok = m < p.M;
-    float sab = sab_all;
-    if (p.a_rows) sab = row_ok ? __fmul_rn(__ldg(p.sinv_a + m), sinv_b) : 0.0f;
-    // Bias of columns nbase + 4 lane .. + 3, read once per tile, handed out by shuffle.
-    float4 bias_l = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.bias != nullptr && lane < C::kWarpCols / 4) {
-      const int c4 = t.nbase + 4 * lane;
-      bias_l.x = c4 < p.N ? __ldg(p.bias + c4) : 0.f;
-      bias_l.y = c4 + 1 < p.N ? __ldg(p.bias + c4 + 1) : 0.f;
-      bias_l.z = c4 + 2 < p.N ? __ldg(p.bias + c4 + 2) : 0.f;
-      bias_l.w = c4 + 3 < p.N ? __ldg(p.bias + c4 + 3) : 0.f;
-    }
+    __syncwarp();
+    const uint32_t tbase = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + part * 64);
+    uint32_t r[16];
+    if (cols > 0) tmem_ld16_nowait(tbase, r);
+    // Not unrolled: the body stays in the instruction cache's first level.
 #pragma unroll 1
-    for (int c = 0; c < t.chunks; ++c) {
-      const int n0 = t.nbase + 32 * c;
-      const uint32_t buf = bufs + slot * kStagingBytes;
-      const uint32_t zbuf = bufs + (slot == kActBufs - 1 ? 0u : slot + 1u) * kStagingBytes;
-      uint32_t r[32];
-      __syncwarp();
-      tmem_ld32_nowait(tbase + uint32_t(32 * c), r);
-      if (lane == 0) {  // one group per chunk
-        if (p.z != nullptr) bulk_wait_read_all();
-        else bulk_wait_read_le1();
-      }
-      __syncwarp();
-      ask();
-      uint32_t aux[16];
-      if (p.aux != nullptr) {
-        if (p.aux_tma) {
-          ok = mbar_wait(aux_bar + 8u * slot, parity, abort, p.err, kWaitEpilogueAux, p.wait_ns);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-        } else {
-          const bool col_ok = n0 + lane < p.N;
-          const uint16_t* src = p.aux + int64_t(t.m0) * p.N + n0 + lane;
-#pragma unroll 16
-          for (int rr = 0; rr < 32; ++rr) {
-            const uint16_t a16 = col_ok && t.m0 + rr < p.M ? src[int64_t(rr) * p.N] : uint16_t(0);
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(unit64(buf, rr, lane >> 3) + uint32_t((lane & 7) << 1)),
-                         "h"(a16)
-                         : "memory");
-          }
-          __syncwarp();
+    for (int h = 0; 16 * h < cols; ++h) {
+      tmem_wait_ld16(r);
+      float y[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(r[j]);
+      if (16 * (h + 1) < cols) tmem_ld16_nowait(tbase + uint32_t(16 * (h + 1)), r);
+      if (p.bias != nullptr) {  // warp-uniform
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float b0 = __shfl_sync(0xFFFFFFFFu, bias_l.x, 8 * h + j / 2);
+          const float b1 = __shfl_sync(0xFFFFFFFFu, bias_l.y, 8 * h + j / 2);
+          fma2(y[j], y[j + 1], sab, b0, b1);
         }
+      } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(aux[4 * u]), "=r"(aux[4 * u + 1]), "=r"(aux[4 * u + 2]), "=r"(aux[4 * u + 3])
-                       : "r"(unit64(buf, lane, u))
-                       : "memory");
-      }
-      tmem_wait_ld();
-      if (c + 1 == t.chunks) release();
-      if (!ok) break;
-      float y[32];
-#pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.bias != nullptr) {  // warp-uniform
-          const int src = 8 * c + j / 4;
-          bv.x = __shfl_sync(0xFFFFFFFFu, bias_l.x, src);
-          bv.y = __shfl_sync(0xFFFFFFFFu, bias_l.y, src);
-          bv.z = __shfl_sync(0xFFFFFFFFu, bias_l.z, src);
-          bv.w = __shfl_sync(0xFFFFFFFFu, bias_l.w, src);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[j + e] = __uint_as_float(r[j + e]);
-        fma2(y[j], y[j + 1], sab, bv.x, bv.y);
-        fma2(y[j + 2], y[j + 3], sab, bv.z, bv.w);
+        for (int j = 0; j < 16; j += 2) scale2(y[j], y[j + 1], sab);
       }
       auto pack = [&](int j) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(y[j], y[j + 1]);
-        return *reinterpret_cast<const uint32_t*>(&h);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(y[j], y[j + 1]);
+        return *reinterpret_cast<const uint32_t*>(&v);
       };
-      if (p.z != nullptr) {
+      uint32_t aux[8];
+      if (has_aux) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          st_shared16(unit64(zbuf, lane, u), pack(8 * u), pack(8 * u + 2), pack(8 * u + 4), pack(8 * u + 6));
+        for (int u = 0; u < 2; ++u)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(aux[4 * u]), "=r"(aux[4 * u + 1]), "=r"(aux[4 * u + 2]), "=r"(aux[4 * u + 3])
+                       : "r"(unit128(bufa, lane, 2 * h + u))
+                       : "memory");
+      }
+      if (has_z) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          st_shared16(unit128(zbuf, lane, 2 * h + u), pack(8 * u), pack(8 * u + 2), pack(8 * u + 4), pack(8 * u + 6));
       }
       switch (p.act) {  // warp-uniform
-        case FP8_ACT_RELU: act_chunk<FP8_ACT_RELU>(y); break;
-        case FP8_ACT_GELU: act_chunk<FP8_ACT_GELU>(y); break;
-        case FP8_ACT_SILU: act_chunk<FP8_ACT_SILU>(y); break;
+        case FP8_ACT_RELU: act16<FP8_ACT_RELU>(y); break;
+        case FP8_ACT_GELU: act16<FP8_ACT_GELU>(y); break;
+        case FP8_ACT_SILU: act16<FP8_ACT_SILU>(y); break;
         default: break;
       }
-      if (p.aux != nullptr) {
+      if (has_aux) {
         if (p.aux_mul) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
+          for (int j = 0; j < 8; ++j)
             mul2(y[2 * j], y[2 * j + 1], __uint_as_float(aux[j] << 16), __uint_as_float(aux[j] & 0xFFFF0000u));
         } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
+          for (int j = 0; j < 8; ++j)
             add2(y[2 * j], y[2 * j + 1], __uint_as_float(aux[j] << 16), __uint_as_float(aux[j] & 0xFFFF0000u));
         }
       }
       if constexpr (kOut8) {
         // Columns beyond N hold act(0) and aux 0, hence y = 0; rows beyond M do not count.
-        if (row_ok) {
+        float m16 = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) amax = fmaxf(amax, fmaxf(fabsf(y[j]), fabsf(y[j + 1])));
-        }
-        uint32_t code[8];
-        if (p.out_fmt == FP8_E5M2) {
+        for (int j = 0; j < 16; j += 2) m16 = fmaxf(m16, fmaxf(fabsf(y[j]), fabsf(y[j + 1])));
+        if (row_ok) amax = fmaxf(amax, m16);
+        uint32_t code[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) code[j] = cvt4<FP8_E5M2>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) code[j] = cvt4<FP8_E4M3>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out);
-        }
-        // 32 x 32 codes in the first 1 KB, 32B swizzle: 16-byte unit u of row
-        // r at unit u ^ ((r >> 2) & 1).  They lie over other lanes' aux rows.
-        __syncwarp();
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          st_shared16(buf + uint32_t(lane) * 32u + uint32_t((u ^ ((lane >> 2) & 1)) * 16), code[4 * u], code[4 * u + 1],
-                      code[4 * u + 2], code[4 * u + 3]);
+        for (int j = 0; j < 4; ++j)
+          code[j] = p.out_fmt == FP8_E5M2 ? cvt4<FP8_E5M2>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out)
+                                          : cvt4<FP8_E4M3>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out);
+        st_shared16(unit64(bufb, lane, h), code[0], code[1], code[2], code[3]);
       } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          st_shared16(unit64(buf, lane, u), pack(8 * u), pack(8 * u + 2), pack(8 * u + 4), pack(8 * u + 6));
-      }
-      if (!p.tma_store || (p.z != nullptr && !p.z_tma)) {
-        // Rows that TMA cannot write: lane l takes column n0 + l of every row.
-        __syncwarp();
-        const bool col_ok = n0 + lane < p.N;
-        const int64_t o = int64_t(t.m0) * p.N + n0 + lane;
-#pragma unroll 4
-        for (int rr = 0; rr < 32; ++rr) {
-          if (!col_ok || t.m0 + rr >= p.M) continue;
-          uint16_t v;
-          if (p.z != nullptr && !p.z_tma) {
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(unit64(zbuf, rr, lane >> 3) + uint32_t((lane & 7) << 1)) : "memory");
-            p.z[o + int64_t(rr) * p.N] = v;
-          }
-          if (!p.tma_store) {
-            if constexpr (kOut8) {
-              asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(buf + uint32_t(rr) * 32u + uint32_t((((lane >> 4) ^ ((rr >> 2) & 1)) << 4) + (lane & 15))) : "memory");
-              p.out8[o + int64_t(rr) * p.N] = uint8_t(v);
-            } else {
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(unit64(buf, rr, lane >> 3) + uint32_t((lane & 7) << 1)) : "memory");
-              p.out[o + int64_t(rr) * p.N] = v;
-            }
-          }
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if (p.z != nullptr && p.z_tma) tma_store_3d(tmZ, zbuf, n0, t.m0, 0);
-        if (p.tma_store) tma_store_3d(tmC, buf, n0, t.m0, 0);
-        bulk_commit();
-      }
-      slot = next_slot(slot);
-      if (++turn == kActBufs) {
-        turn = 0;
-        parity ^= 1u;
+        for (int u = 0; u < 2; ++u)
+          st_shared16(unit128(bufa, lane, 2 * h + u), pack(8 * u), pack(8 * u + 2), pack(8 * u + 4), pack(8 * u + 6));
       }
     }
+    // Last TMEM read of this tile for this warp: hand the accumulator back.
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(PAIR == 1 ? tempty0 + 8u * acc : mapa_shared(tempty0 + 8u * acc, 0));
+    if (!t.any) continue;
+    if (has_z && !p.z_tma) store_rows_bf16(p, p.z, zbuf, t, lane);
+    if (!p.tma_store) {
+      if constexpr (kOut8) store_rows_codes(p, bufb, t, lane);
+      else store_rows_bf16(p, p.out, bufa, t, lane);
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (has_z && p.z_tma) tma_store_3d(tmZ, zbuf, t.n0, t.m0, 0);
+      if (p.tma_store) tma_store_3d(tmC, kOut8 ? bufb : bufa, t.n0, t.m0, 0);
+      bulk_commit();
+      bulk_wait_read_all();
+    }
+    __syncwarp();
+    if (prefetch) ask();
   }
-  if (lane == 0) {
-    // Loads asked for and not consumed (only after a wait gave up, at most two)
-    // land before shared memory is released; stores have read it.
-    for (; prefetch && slot != pslot; slot = next_slot(slot)) {
-      const unsigned long long t0 = globaltimer_ns();
-      while (!mbar_try_wait(aux_bar + 8u * slot, parity) && globaltimer_ns() - t0 < kWaitBudgetNs) {
-      }
-      if (++turn == kActBufs) {
-        turn = 0;
-        parity ^= 1u;
-      }
+  if (lane == 0 && asked) {
+    // Asked for and not consumed (only after a wait gave up): it lands before
+    // shared memory is released.
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait(aux_bar, aux_par) && globaltimer_ns() - t0 < kWaitBudgetNs) {
     }
-    bulk_wait_read_all();
   }
   __syncwarp();
   return amax;
@@ -782,7 +796,7 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
                                         const MmParams& p, const int cta, const int ctas,
                                         const CUtensorMap* tmX = nullptr, const CUtensorMap* tmZ = nullptr) {
   constexpr bool kAct = (EPI & kEpiAct) != 0;
-  using C = std::conditional_t<kAct, ActCfg<BN, PAIR>, Cfg<BN, PAIR>>;
+  using C = std::conditional_t<kAct, ActCfg<BN, PAIR, EPI>, Cfg<BN, PAIR>>;
   constexpr int kEW = C::kWarps;  // epilogue warps
   constexpr bool kOut8 = (EPI & kEpiOut8) != 0;
   constexpr bool kBias8 = (EPI & kEpiBias8) != 0;
@@ -824,7 +838,7 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
     mbar_init(done_bar, 1);
     mbar_init(stall_bar, 1);
     if constexpr (kAct) {
-      for (int k = 0; k < kActBufs * kEW; ++k) mbar_init(bar0 + 256u + 8u * k, 1);
+      for (int k = 0; k < kEW; ++k) mbar_init(bar0 + 256u + 8u * k, 1);
     }
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -973,7 +987,7 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
     }
     __syncwarp();
   } else if constexpr (kAct) {
-    const float amax_l = act_epilogue<BN, PAIR, kOut8>(tmC, tmX, tmZ, p, cta, ctas, rank, warp - 2, warp & 3, lane,
+    const float amax_l = act_epilogue<BN, PAIR, EPI>(tmC, tmX, tmZ, p, cta, ctas, rank, warp - 2, warp & 3, lane,
                                                        sbase + C::kStagingOffset, tmem_base, bar0, abort);
     if constexpr (kOut8) {
       float amax = amax_l;
@@ -1330,11 +1344,11 @@ __global__ void __launch_bounds__(kThreadsMM, 1)
 
 // The product with an activation epilogue.
 template <int BN, int PAIR, int EPI>
-__global__ void __launch_bounds__(ActCfg<BN, PAIR>::kThreads, 1)
+__global__ void __launch_bounds__(ActCfg<BN, PAIR, EPI>::kThreads, 1)
     mm_act_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmX,
                   const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ MmParams p) {
-  mm_body<BN, PAIR, EPI | kEpiAct>(&tmA, &tmB, &tmC, p, int(blockIdx.x) / PAIR, int(gridDim.x) / PAIR, &tmX, &tmZ);
+  mm_body<BN, PAIR, EPI>(&tmA, &tmB, &tmC, p, int(blockIdx.x) / PAIR, int(gridDim.x) / PAIR, &tmX, &tmZ);
 }
 
 // Two independent GEMMs in one persistent launch (the dX and dW GEMMs of a
@@ -1493,6 +1507,17 @@ bool make_out_map(CUtensorMap* m, uint16_t* base, int64_t M, int64_t N, int64_t 
                              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
+// Map over a bf16 or code matrix [M, N] with 32 x 64 boxes in the activation
+// epilogue's buffer layouts.
+bool make_act_map(CUtensorMap* m, const void* base, int64_t M, int64_t N, int bytes) {
+  const uint64_t dims[3] = {uint64_t(N), uint64_t(M), 1};
+  const uint64_t strides[2] = {uint64_t(N) * bytes, uint64_t(M) * uint64_t(N) * bytes};
+  const uint32_t box[3] = {64u, 32u, 1u};
+  return encode_tiled_cached(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base,
+                             dims, strides, box, bytes == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                             CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
 int sm_count() {
   static int cached[64] = {0};
   int dev = 0;
@@ -1640,27 +1665,32 @@ int launch_act_epi(const MmProblem& q, const MmChoice& c, cudaStream_t st) {
   MmParams p = q.p;
   const int rc = prepare_mm<BN, PAIR>(q.A, q.B, q.M, q.N, q.K, 1, nullptr, p, c, nullptr, ta, tb, tc);
   if (rc != FP8_OK) return rc;
+  p.inv_span = 1.0f / float(8 * p.n_tiles);
   memset(&tx, 0, sizeof(tx));
   memset(&tz, 0, sizeof(tz));
-  if (p.aux_tma && !make_out_map(&tx, const_cast<uint16_t*>(p.aux), q.M, q.N, 1, q.M * q.N)) return FP8_ERR_CUDA;
-  if (p.z_tma && !make_out_map(&tz, p.z, q.M, q.N, 1, q.M * q.N)) return FP8_ERR_CUDA;
+  if (p.tma_store && !make_act_map(&tc, p.out8 != nullptr ? static_cast<void*>(p.out8) : p.out, q.M, q.N, p.out8 ? 1 : 2))
+    return FP8_ERR_CUDA;
+  if (p.aux_tma && !make_act_map(&tx, p.aux, q.M, q.N, 2)) return FP8_ERR_CUDA;
+  if (p.z_tma && !make_act_map(&tz, p.z, q.M, q.N, 2)) return FP8_ERR_CUDA;
   static bool done[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8_ERR_CUDA;
   if (!done[dev]) {
     if (cudaFuncSetAttribute(mm_act_kernel<BN, PAIR, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             ActCfg<BN, PAIR>::kSmemBytes) != cudaSuccess)
+                             ActCfg<BN, PAIR, EPI>::kSmemBytes) != cudaSuccess)
       return FP8_ERR_CUDA;
     done[dev] = true;
   }
-  const cudaError_t e = launch_pdl(mm_act_kernel<BN, PAIR, EPI>, dim3(PAIR * std::max(1, c.grid)), dim3(ActCfg<BN, PAIR>::kThreads),
-                                   ActCfg<BN, PAIR>::kSmemBytes, st, PAIR, ta, tb, tc, tx, tz, p);
+  const cudaError_t e = launch_pdl(mm_act_kernel<BN, PAIR, EPI>, dim3(PAIR * std::max(1, c.grid)), dim3(ActCfg<BN, PAIR, EPI>::kThreads),
+                                   ActCfg<BN, PAIR, EPI>::kSmemBytes, st, PAIR, ta, tb, tc, tx, tz, p);
   return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
 template <int BN, int PAIR>
 int launch_act(const MmProblem& q, const MmChoice& c, cudaStream_t st) {
-  return q.epi & kEpiOut8 ? launch_act_epi<BN, PAIR, kEpiOut8>(q, c, st) : launch_act_epi<BN, PAIR, 0>(q, c, st);
+  if (q.epi & kEpiOut8) return launch_act_epi<BN, PAIR, kEpiAct | kEpiOut8>(q, c, st);
+  return q.p.z != nullptr ? launch_act_epi<BN, PAIR, kEpiAct | kEpiZ>(q, c, st)
+                          : launch_act_epi<BN, PAIR, kEpiAct>(q, c, st);
 }
 
 template <int BN, int PAIR>
