@@ -70,12 +70,9 @@ __device__ __forceinline__ void act_value_slope(int act, float z, float& value, 
 
 // ---- two values at a time, for the product's epilogue ------------------------
 //
-// There the eight epilogue warps have about 36 issue slots per element while
-// the next tile's products run, so each operation that can is a packed one and
-// one reciprocal serves two values: 1/x = y r, 1/y = x r with r = 1/(x y).
-// z is held at or above a floor first (-41 for silu, -7.4 for gelu, where the
-// value is within 2^-53 of 0), so that x and y stay below 2^60: no overflow,
-// and a huge negative z gives 0.
+// The epilogue's warps have some 20 issue slots per element while the next
+// tile's products run, so each operation that can is a packed one.  e^-w grows
+// without bound for w << 0: its sum's reciprocal is then 0, and so is the value.
 
 __device__ __forceinline__ void mul2(float& a, float& b, float c, float d) {
   asm("{\n\t.reg .b64 ra, rc;\n\t"
@@ -123,11 +120,8 @@ __device__ __forceinline__ void act_pair(float& a, float& b) {
     a = max_nan(a, 0.0f);
     b = max_nan(b, 0.0f);
   } else {
-    constexpr bool kGelu = ACT == FP8_ACT_GELU;
-    a = max_nan(a, kGelu ? -7.4f : -41.0f);
-    b = max_nan(b, kGelu ? -7.4f : -41.0f);
-    float x = a, y = b;  // -> 2^(-w log2 e) + 1
-    if constexpr (kGelu) {
+    float x = a, y = b;  // -> e^-w + 1
+    if constexpr (ACT == FP8_ACT_GELU) {
       constexpr float c1 = -kGeluC2 * kLog2E;
       mul2(x, y, a, b);
       fma2(x, y, c1 * kGeluA, c1, c1);
@@ -138,8 +132,7 @@ __device__ __forceinline__ void act_pair(float& a, float& b) {
     x = exp2_fast(x);
     y = exp2_fast(y);
     add2(x, y, 1.0f, 1.0f);
-    const float r = rcp_fast(x * y);
-    mul2(a, b, r * y, r * x);
+    mul2(a, b, rcp_fast(x), rcp_fast(y));
   }
 }
 

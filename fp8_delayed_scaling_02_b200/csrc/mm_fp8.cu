@@ -276,6 +276,9 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, uint32_t src
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ void ld_shared16(uint32_t addr, uint32_t* v) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read_le1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 // Every bulk store of this thread has finished reading shared memory (its
@@ -626,6 +629,10 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
   const bool has_z = kOut8 ? p.z != nullptr : (EPI & kEpiZ) != 0;
   // z lies over the aux units when codes leave, beside them when y does.
   const uint32_t zbuf = kOut8 ? bufa : bufb;
+  // This lane's row of the buffers (unit128's and unit64's layout).
+  const uint32_t rowa = bufa + uint32_t(lane) * 128u, rowz = zbuf + uint32_t(lane) * 128u;
+  const uint32_t rowb = bufb + uint32_t(lane) * 64u;
+  const uint32_t swz = uint32_t(lane & 7) * 16u, swz8 = uint32_t((lane >> 1) & 3) * 16u;
   const float sinv_b = *p.sinv_b;
   const float sab_all = __fmul_rn(*p.sinv_a, sinv_b);
   const float s_out = kOut8 ? *p.r_scale : 0.0f;
@@ -683,16 +690,20 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
     tc_fence_after();
     __syncwarp();
     const uint32_t tbase = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + part * 64);
-    uint32_t r[16];
-    if (cols > 0) tmem_ld16_nowait(tbase, r);
     // Not unrolled: the body stays in the instruction cache's first level.
 #pragma unroll 1
     for (int h = 0; 16 * h < cols; ++h) {
+      uint32_t r[16];
+      tmem_ld16_nowait(tbase + uint32_t(16 * h), r);
+      uint32_t aux[8];
+      if (has_aux) {
+        ld_shared16(rowa + (uint32_t(32 * h) ^ swz), aux);
+        ld_shared16(rowa + (uint32_t(32 * h + 16) ^ swz), aux + 4);
+      }
       tmem_wait_ld16(r);
       float y[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(r[j]);
-      if (16 * (h + 1) < cols) tmem_ld16_nowait(tbase + uint32_t(16 * (h + 1)), r);
       if (p.bias != nullptr) {  // warp-uniform
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
@@ -708,19 +719,9 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
         const __nv_bfloat162 v = __floats2bfloat162_rn(y[j], y[j + 1]);
         return *reinterpret_cast<const uint32_t*>(&v);
       };
-      uint32_t aux[8];
-      if (has_aux) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(aux[4 * u]), "=r"(aux[4 * u + 1]), "=r"(aux[4 * u + 2]), "=r"(aux[4 * u + 3])
-                       : "r"(unit128(bufa, lane, 2 * h + u))
-                       : "memory");
-      }
       if (has_z) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          st_shared16(unit128(zbuf, lane, 2 * h + u), pack(8 * u), pack(8 * u + 2), pack(8 * u + 4), pack(8 * u + 6));
+        st_shared16(rowz + (uint32_t(32 * h) ^ swz), pack(0), pack(2), pack(4), pack(6));
+        st_shared16(rowz + (uint32_t(32 * h + 16) ^ swz), pack(8), pack(10), pack(12), pack(14));
       }
       switch (p.act) {  // warp-uniform
         case FP8_ACT_RELU: act16<FP8_ACT_RELU>(y); break;
@@ -750,11 +751,10 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
         for (int j = 0; j < 4; ++j)
           code[j] = p.out_fmt == FP8_E5M2 ? cvt4<FP8_E5M2>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out)
                                           : cvt4<FP8_E4M3>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out);
-        st_shared16(unit64(bufb, lane, h), code[0], code[1], code[2], code[3]);
+        st_shared16(rowb + (uint32_t(16 * h) ^ swz8), code[0], code[1], code[2], code[3]);
       } else {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          st_shared16(unit128(bufa, lane, 2 * h + u), pack(8 * u), pack(8 * u + 2), pack(8 * u + 4), pack(8 * u + 6));
+        st_shared16(rowa + (uint32_t(32 * h) ^ swz), pack(0), pack(2), pack(4), pack(6));
+        st_shared16(rowa + (uint32_t(32 * h + 16) ^ swz), pack(8), pack(10), pack(12), pack(14));
       }
     }
     // Last TMEM read of this tile for this warp: hand the accumulator back.

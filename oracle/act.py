@@ -48,11 +48,11 @@ def value_error(z, kind):
 
     e^-|w| by the fast exponential: 2 + 1.2 |w| ulp, one ulp at most 2 U; w
     itself (gelu) rounds four times, 4 U |w| in the exponent; 1 + t and the
-    final products once each, the fast division 2 ulp.  Below a floor (-41 for
-    silu, -7.4 for gelu) a kernel may give the floor's value, under 2^-53.
+    final products once each, the fast division 2 ulp.  Where e^-w leaves
+    float32's range, the value, below 2^-119, may be 0.
     """
     z = np.asarray(z, dtype=np.float64)
-    return np.abs(act(z, kind)) * _relative(z, kind) + (2.0 ** -53 if kind in (GELU, SILU) else 0.0)
+    return np.abs(act(z, kind)) * _relative(z, kind) + 2.0 ** -119
 
 
 def slope_error(z, kind):
