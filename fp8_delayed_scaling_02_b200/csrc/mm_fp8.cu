@@ -266,6 +266,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
       : "memory");
 }
 
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* tm, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
 // Bulk tensor store of a shared-memory box; clipped to the tensor bounds.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, uint32_t src, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -643,18 +651,26 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
   // The piece whose aux has been asked for, or is to be next.
   ActPiece nx{-1, 0, 0, false};
   bool asked = false;
-  auto ask = [&]() {  // warp-uniform; lane 0 issues
-    asked = false;
+  auto find = [&]() {  // warp-uniform
     do {
-      if (!act_piece<BN, PAIR>(p, cta, ctas, rank, quad, part, nx.i + 1, nx)) return;
+      if (!act_piece<BN, PAIR>(p, cta, ctas, rank, quad, part, nx.i + 1, nx)) {
+        nx.any = false;
+        return;
+      }
     } while (!nx.any);
-    asked = true;
-    if (lane == 0) {
+    if (lane == 0) tma_prefetch_3d(tmX, nx.n0, nx.m0, 0);
+  };
+  auto ask = [&]() {  // lane 0 issues
+    asked = nx.any;
+    if (asked && lane == 0) {
       mbar_arrive_expect_tx(aux_bar, C::kBufA);
       tma_load_3d(bufa, tmX, nx.n0, nx.m0, 0, aux_bar);
     }
   };
-  if (prefetch) ask();
+  if (prefetch) {
+    find();
+    ask();
+  }
   uint32_t aux_par = 0;
   ActPiece t;
   for (int i = 0; act_piece<BN, PAIR>(p, cta, ctas, rank, quad, part, i, t); ++i) {
@@ -676,6 +692,7 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
         if (!ok) break;
         asked = false;
         aux_par ^= 1u;
+        find();  // into L2 by the time this buffer is free
       } else {
         load_rows_bf16(p, bufa, t, lane);
         __syncwarp();
