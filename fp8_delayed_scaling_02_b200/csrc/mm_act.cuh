@@ -27,6 +27,7 @@ struct SkinnyArgs {
 
 constexpr int kSkinnyMaxM = 32;
 
-int launch_skinny(const SkinnyArgs& a, cudaStream_t st);  // 1 <= M <= kSkinnyMaxM
+bool skinny_wins(int64_t M, int64_t N, int sms);
+int launch_skinny(const SkinnyArgs& a, int sms, cudaStream_t st);  // 1 <= M <= kSkinnyMaxM
 
 }  // namespace fp8ds

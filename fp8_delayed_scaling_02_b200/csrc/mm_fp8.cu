@@ -2098,17 +2098,17 @@ extern "C" int fp8_mm_act(const fp8_mm_act_args* a, fp8_stream_t stream) {
   if (q.K == 0)
     return launch_pdl(mm_act_k0_kernel, dim3(1), dim3(256), 0, st, 1, p, q.M, q.N) == cudaSuccess ? FP8_OK
                                                                                                  : FP8_ERR_CUDA;
-  if (q.M <= kSkinnyMaxM) {
+  const int sms = sm_count();
+  if (sms <= 0) return FP8_ERR_CUDA;
+  if (skinny_wins(q.M, q.N, sms)) {
     SkinnyArgs s{a->A, a->B, p.M, p.N, p.K, a->layout & FP8_MM_A_E5M2 ? FP8_E5M2 : FP8_E4M3,
                  a->layout & FP8_MM_B_E5M2 ? FP8_E5M2 : FP8_E4M3, a->sinv_a, p.a_rows, a->sinv_b, a->bias, p.act, p.aux,
                  p.aux_mul, p.z, p.out, p.out8, p.out_fmt, RingArgs{}};
     if (out8)
       s.ring = RingArgs{a->out_ring.history, a->out_ring.idx, a->out_ring.scale, a->out_ring.scale_inv,
                         a->out_ring.scratch, a->out_amax};
-    return launch_skinny(s, st);
+    return launch_skinny(s, sms, st);
   }
-  const int sms = sm_count();
-  if (sms <= 0) return FP8_ERR_CUDA;
   const MmChoice c = choose_mm(q.M, q.N, q.K, 1, sms, false, 0);
   if (c.pair == 2) return launch_act<256, 2>(q, c, st);
   if (c.bn == 256) return launch_act<256, 1>(q, c, st);

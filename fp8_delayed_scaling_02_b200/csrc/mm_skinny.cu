@@ -30,8 +30,6 @@ namespace {
 
 constexpr int kSkThreads = 256;
 constexpr int kSkWarps = kSkThreads / 32;
-constexpr int kSkRows = 16;   // rows of B per block
-constexpr int kSkUnroll = 4;  // steps of 64 bytes in flight per warp
 
 template <int FA, int FB>
 __device__ __forceinline__ void mma_f8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -48,67 +46,76 @@ __device__ __forceinline__ void mma_f8(float (&c)[4], uint32_t a0, uint32_t a1, 
 #undef FP8DS_MMA
 }
 
-// NT: groups of eight tokens.  FB is the format of B, the MMA's row operand.
-template <int FA, int FB, int NT, bool kOut8>
+// NT: groups of eight tokens.  RG: groups of sixteen rows of B per block.  FB is the format of B, the MMA's row operand.
+template <int FA, int FB, int NT, int RG, bool kOut8>
 __global__ void __launch_bounds__(kSkThreads) mm_skinny_kernel(const __grid_constant__ SkinnyArgs p) {
+  constexpr int kUnroll = RG * NT >= 4 ? 2 : 4;  // steps of 64 bytes in flight per warp
   constexpr int kPitch = 8 * NT + 4;  // floats between rows of the partial sums: conflict-free for the fragments
-  __shared__ float red[kSkWarps][kSkRows][kPitch];
+  __shared__ float red[kSkWarps][16 * RG][kPitch];
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int n0 = int(blockIdx.x) * kSkRows;
+  const int n0 = int(blockIdx.x) * 16 * RG;
   const float s_out = kOut8 ? *p.ring.scale : 0.0f;
   RingCache rc{0.0f, 0};
   if constexpr (kOut8) rc = prefetch_ring(p.ring);
 
-  float acc[NT][4];
+  float acc[RG][NT][4];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-  const uint8_t* b0p = p.B + int64_t(n0 + g) * p.K + 16 * t;
-  const uint8_t* b1p = b0p + int64_t(8) * p.K;
+  for (int q = 0; q < RG; ++q)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[q][j][0] = acc[q][j][1] = acc[q][j][2] = acc[q][j][3] = 0.0f;
+  const uint8_t* bp = p.B + int64_t(n0 + g) * p.K + 16 * t;
   const uint8_t* ap = p.A + int64_t(g) * p.K + 16 * t;
-  const bool b0_ok = n0 + g < p.N, b1_ok = n0 + g + 8 < p.N;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const int steps = (p.K + 63) / 64;
-  for (int s0 = warp; s0 < steps; s0 += kSkWarps * kSkUnroll) {
-    uint4 wb0[kSkUnroll], wb1[kSkUnroll], wa[kSkUnroll][NT];
+  for (int s0 = warp; s0 < steps; s0 += kSkWarps * kUnroll) {
+    uint4 wb[kUnroll][2 * RG], wa[kUnroll][NT];  // rows g, g + 8, g + 16, ...; tokens g, g + 8, ...
 #pragma unroll
-    for (int u = 0; u < kSkUnroll; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       const int k = 64 * (s0 + u * kSkWarps);
       const bool k_ok = k + 16 * t < p.K;
-      wb0[u] = b0_ok && k_ok ? __ldg(reinterpret_cast<const uint4*>(b0p + k)) : zero;
-      wb1[u] = b1_ok && k_ok ? __ldg(reinterpret_cast<const uint4*>(b1p + k)) : zero;
+#pragma unroll
+      for (int q = 0; q < 2 * RG; ++q)
+        wb[u][q] = k_ok && n0 + g + 8 * q < p.N
+                       ? __ldg(reinterpret_cast<const uint4*>(bp + int64_t(8 * q) * p.K + k)) : zero;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
         wa[u][j] = k_ok && 8 * j + g < p.M ? __ldg(reinterpret_cast<const uint4*>(ap + int64_t(8 * j) * p.K + k)) : zero;
     }
 #pragma unroll
-    for (int u = 0; u < kSkUnroll; ++u)
+    for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        mma_f8<FB, FA>(acc[j], wb0[u].x, wb1[u].x, wb0[u].y, wb1[u].y, wa[u][j].x, wa[u][j].y);
-        mma_f8<FB, FA>(acc[j], wb0[u].z, wb1[u].z, wb0[u].w, wb1[u].w, wa[u][j].z, wa[u][j].w);
+      for (int q = 0; q < RG; ++q) {
+        const uint4 lo = wb[u][2 * q], hi = wb[u][2 * q + 1];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_f8<FB, FA>(acc[q][j], lo.x, hi.x, lo.y, hi.y, wa[u][j].x, wa[u][j].y);
+          mma_f8<FB, FA>(acc[q][j], lo.z, hi.z, lo.w, hi.w, wa[u][j].z, wa[u][j].w);
+        }
       }
   }
-  // acc[j]: rows g and g + 8 of B, tokens 8j + 2t and + 1.
+  // acc[q][j]: rows 16q + g and + 8 of B, tokens 8j + 2t and + 1.
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    red[warp][g][8 * j + 2 * t] = acc[j][0];
-    red[warp][g][8 * j + 2 * t + 1] = acc[j][1];
-    red[warp][g + 8][8 * j + 2 * t] = acc[j][2];
-    red[warp][g + 8][8 * j + 2 * t + 1] = acc[j][3];
-  }
+  for (int q = 0; q < RG; ++q)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      red[warp][16 * q + g][8 * j + 2 * t] = acc[q][j][0];
+      red[warp][16 * q + g][8 * j + 2 * t + 1] = acc[q][j][1];
+      red[warp][16 * q + g + 8][8 * j + 2 * t] = acc[q][j][2];
+      red[warp][16 * q + g + 8][8 * j + 2 * t + 1] = acc[q][j][3];
+    }
   __syncthreads();
 
   float amax = 0.0f;
-  const int n = n0 + (threadIdx.x & 15);
+  const int col = threadIdx.x % (16 * RG), n = n0 + col;
   const float sinv_b = *p.sinv_b;
   const float bias = p.bias != nullptr && n < p.N ? __ldg(p.bias + n) : 0.0f;
-  for (int m = threadIdx.x >> 4; m < p.M; m += kSkThreads / 16) {
+  for (int m = threadIdx.x / (16 * RG); m < p.M; m += kSkThreads / (16 * RG)) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kSkWarps; ++w) v += red[w][threadIdx.x & 15][m];
+    for (int w = 0; w < kSkWarps; ++w) v += red[w][col][m];
     if (n < p.N) {
       const int64_t o = int64_t(m) * p.N + n;
       const float sab = __fmul_rn(p.sinv_a[p.a_rows ? m : 0], sinv_b);
@@ -133,28 +140,41 @@ __global__ void __launch_bounds__(kSkThreads) mm_skinny_kernel(const __grid_cons
   }
 }
 
-template <int FA, int FB, int NT>
-cudaError_t launch_nt(const SkinnyArgs& a, cudaStream_t st) {
-  const dim3 grid(unsigned((a.N + kSkRows - 1) / kSkRows));
-  if (a.out8 != nullptr) return launch_pdl(mm_skinny_kernel<FA, FB, NT, true>, grid, dim3(kSkThreads), 0, st, 1, a);
-  return launch_pdl(mm_skinny_kernel<FA, FB, NT, false>, grid, dim3(kSkThreads), 0, st, 1, a);
+template <int FA, int FB, int NT, int RG>
+cudaError_t launch_rg(const SkinnyArgs& a, cudaStream_t st) {
+  const dim3 grid(unsigned((a.N + 16 * RG - 1) / (16 * RG)));
+  if (a.out8 != nullptr) return launch_pdl(mm_skinny_kernel<FA, FB, NT, RG, true>, grid, dim3(kSkThreads), 0, st, 1, a);
+  return launch_pdl(mm_skinny_kernel<FA, FB, NT, RG, false>, grid, dim3(kSkThreads), 0, st, 1, a);
 }
 
+// Two groups of rows where that still leaves a block for every SM: the tokens
+// are read and converted half as often (one token at 8192 x 4096: 7.9 us, one
+// group 8.7; at 4096 x 1536 3.7 and 3.1).
 template <int FA, int FB>
-cudaError_t launch_fmt(const SkinnyArgs& a, cudaStream_t st) {
-  if (a.M <= 8) return launch_nt<FA, FB, 1>(a, st);
-  if (a.M <= 16) return launch_nt<FA, FB, 2>(a, st);
-  return launch_nt<FA, FB, 4>(a, st);
+cudaError_t launch_fmt(const SkinnyArgs& a, int sms, cudaStream_t st) {
+  const bool two = (a.N + 31) / 32 >= sms;
+  if (a.M <= 8) return two ? launch_rg<FA, FB, 1, 2>(a, st) : launch_rg<FA, FB, 1, 1>(a, st);
+  if (a.M <= 16) return two ? launch_rg<FA, FB, 2, 2>(a, st) : launch_rg<FA, FB, 2, 1>(a, st);
+  return launch_rg<FA, FB, 4, 1>(a, st);
 }
 
 }  // namespace
 
-int launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
+// The FP8 mma of mma.sync converts its operands first, at a rate that more
+// tokens soon reach.  Against the tile kernel, at N x K of 1536 x 4096, 4096 x
+// 1536, 4096 x 4096 and 8192 x 4096 (us here / there): 8 tokens 4.8 / 13.9, 3.4 /
+// 8.0, 5.4 / 14.2, 8.5 / 18.7; 16 tokens 6.4 / 13.9, 4.1 / 7.9, 6.7 / 14.2, 15.1 /
+// 18.1; 32 tokens 10.4 / 13.9, 6.5 / 7.9, 11.1 / 14.1, 33.7 / 15.0.
+bool skinny_wins(int64_t M, int64_t N, int sms) {
+  return M <= 16 || (M <= kSkinnyMaxM && (N + 15) / 16 <= 2 * int64_t(sms));
+}
+
+int launch_skinny(const SkinnyArgs& a, int sms, cudaStream_t st) {
   cudaError_t e;
   if (a.fmt_a == FP8_E4M3)
-    e = a.fmt_b == FP8_E4M3 ? launch_fmt<FP8_E4M3, FP8_E4M3>(a, st) : launch_fmt<FP8_E4M3, FP8_E5M2>(a, st);
+    e = a.fmt_b == FP8_E4M3 ? launch_fmt<FP8_E4M3, FP8_E4M3>(a, sms, st) : launch_fmt<FP8_E4M3, FP8_E5M2>(a, sms, st);
   else
-    e = a.fmt_b == FP8_E4M3 ? launch_fmt<FP8_E5M2, FP8_E4M3>(a, st) : launch_fmt<FP8_E5M2, FP8_E5M2>(a, st);
+    e = a.fmt_b == FP8_E4M3 ? launch_fmt<FP8_E5M2, FP8_E4M3>(a, sms, st) : launch_fmt<FP8_E5M2, FP8_E5M2>(a, sms, st);
   return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 

@@ -163,31 +163,48 @@ class Ring:
         f[18] = 1.0
 
     @property
+    def buf(self):
+        return self._buf
+
+    @buf.setter
+    def buf(self, t):
+        # The views and addresses below are made on first use and go with the buffer.
+        self.__dict__.clear()
+        self._buf = t
+
+    def __getstate__(self):
+        return {"buf": self._buf}
+
+    def __setstate__(self, state):
+        self.buf = state["buf"]
+
+    @functools.cached_property
     def history(self):
         return self.buf[0:HISTORY_LEN].view(torch.float32)
 
-    @property
+    @functools.cached_property
     def idx(self):
         return self.buf[16:17]
 
-    @property
+    @functools.cached_property
     def scale(self):
         return self.buf[17:18].view(torch.float32)
 
-    @property
+    @functools.cached_property
     def scale_inv(self):
         return self.buf[18:19].view(torch.float32)
 
-    @property
+    @functools.cached_property
     def scratch(self):
         return self.buf[20:24]
 
+    @functools.cached_property
+    def _c(self):
+        base = self.buf.data_ptr()
+        return CRing(base, base + 16 * 4, base + 17 * 4, base + 18 * 4, base + 20 * 4)
+
     def c(self):
-        c = getattr(self, "_c", None)
-        if c is None:
-            base = self.buf.data_ptr()
-            c = self._c = CRing(base, base + 16 * 4, base + 17 * 4, base + 18 * 4, base + 20 * 4)
-        return c
+        return self._c
 
     def state(self):
         """Host copy: (history float32[16], idx, scale, scale_inv, scratch[4])."""
@@ -605,6 +622,9 @@ class Linear:
 # ---- the operators around the linear (include/fp8ds_layer.h) -------------------------
 
 
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
 def _on_stream(fn):
     """Runs ``fn`` with ``stream`` (default: the current one) and its first tensor's device
     current, so that what it allocates and launches belongs to that stream."""
@@ -613,7 +633,7 @@ def _on_stream(fn):
     def call(x, *args, stream=None, **kw):
         if not x.is_cuda:
             raise ValueError("the tensors must be CUDA tensors")
-        if stream is None and x.get_device() == torch.cuda.current_device():
+        if stream is None and x.get_device() == _current_device():
             return fn(x, *args, **kw)
         if stream is not None and stream.device != x.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
@@ -627,23 +647,28 @@ def _same(t, like, name, shape=None, dtype=None):
     """Checks an optional tensor: on ``like``'s device, contiguous, of this shape and type."""
     if t is None:
         return
+    if shape is None:
+        shape = like.shape
+    if dtype is None:
+        dtype = like.dtype
+    if t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device() and t.is_contiguous():
+        return
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    if tuple(t.shape) != tuple(like.shape if shape is None else shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape if shape is None else shape)}")
-    if t.dtype != (like.dtype if dtype is None else dtype):
-        raise ValueError(f"{name} is {t.dtype}, expected {like.dtype if dtype is None else dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _scalar(t, like, name):
-    if t is not None and (t.device != like.device or t.dtype != torch.float32 or t.numel() != 1):
+    if t is not None and (t.get_device() != like.get_device() or t.dtype is not torch.float32 or t.numel() != 1):
         raise ValueError(f"{name} must be a one-element float32 tensor on {like.device}")
 
 
 def _ring_on(ring, like, name):
-    if ring is not None and ring.buf.device != like.device:
+    if ring is not None and ring.buf.get_device() != like.get_device():
         raise ValueError(f"{name} is on {ring.buf.device}, expected {like.device}")
 
 
@@ -710,14 +735,14 @@ def rmsnorm(x, gamma, residual=None, eps=1e-6, fmt=None, ring=None, need_rstd=Fa
         _same(y, x, "y")
     elif need_y or fmt is None:
         y = torch.empty_like(x)
-    rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if need_rstd else None
+    rstd = x.new_empty(rows, dtype=torch.float32) if need_rstd else None
     sinv = row_sinv = None
     if fmt is None:
         if ring is not None or codes is not None or amax is not None:
             raise ValueError("codes, ring and amax need fmt")
     else:
         if codes is None:
-            codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+            codes = torch.empty_like(x, dtype=torch.uint8)
         else:
             _same(codes, x, "codes", None, torch.uint8)
         _scalar(amax, x, "amax")
@@ -727,7 +752,7 @@ def rmsnorm(x, gamma, residual=None, eps=1e-6, fmt=None, ring=None, need_rstd=Fa
         elif amax is not None:
             raise ValueError("amax needs a ring")
         else:
-            sinv = row_sinv = torch.empty(rows, dtype=torch.float32, device=x.device)
+            sinv = row_sinv = x.new_empty(rows, dtype=torch.float32)
     a = CNormArgs(x.data_ptr(), _ptr(residual), IN_DTYPE[x.dtype], rows, cols, gamma.data_ptr(), f32, eps, _ptr(h),
                   _ptr(y), _ptr(rstd), _ptr(codes), fmt or 0, ring.c() if ring is not None else _NO_RING, _ptr(amax),
                   _ptr(row_sinv))
@@ -765,10 +790,10 @@ def rmsnorm_backward(dy, h, rstd, gamma, dres=None, dx=None, need_dgamma=True):
     dgamma = ws = None
     wsb = 0
     if need_dgamma:
-        dgamma = torch.empty(cols, dtype=torch.float32, device=h.device)
+        dgamma = h.new_empty(cols, dtype=torch.float32)
         wsb = L.fp8_rmsnorm_backward_workspace_bytes(rows, cols)
         if wsb:
-            ws = torch.empty(wsb, dtype=torch.uint8, device=h.device)
+            ws = h.new_empty(wsb, dtype=torch.uint8)
     a = CNormBwdArgs(dy.data_ptr(), h.data_ptr(), _ptr(dres), IN_DTYPE[h.dtype], rows, cols, rstd.data_ptr(),
                      gamma.data_ptr(), f32, dx.data_ptr(), _ptr(dgamma), _ptr(ws), wsb)
     _check(L.fp8_rmsnorm_backward(ctypes.byref(a), _raw_stream(h.get_device())), "fp8_rmsnorm_backward")
@@ -825,13 +850,13 @@ def mm_act(a, b, sinv_a, sinv_b, act=ACT_NONE, bias=None, aux=None, aux_op=AUX_A
         _ring_on(out_ring, a, "out_ring")
         kind, dtype = (MM_OUT_E4M3 if out_fmt == E4M3 else MM_OUT_E5M2 if out_fmt == E5M2 else -1), torch.uint8
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=a.device)
+        out = a.new_empty((M, N), dtype=dtype)
     else:
         _same(out, a, "out", (M, N), dtype)
     if z is not None:
         _same(z, a, "z", (M, N), torch.bfloat16)
     elif need_z:
-        z = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+        z = a.new_empty((M, N), dtype=torch.bfloat16)
     args = CMmActArgs(a.data_ptr(), b.data_ptr(), M, N, K,
                       (MM_A_E5M2 if fmt_a == E5M2 else 0) | (MM_B_E5M2 if fmt_b == E5M2 else 0), sinv_a.data_ptr(),
                       1 if na != 1 else 0, sinv_b.data_ptr(), _ptr(bias), act, _ptr(aux), aux_op, _ptr(z), kind,
@@ -884,19 +909,18 @@ def act_backward(dy, z, act, fmt, ring, u=None, ring_u=None, need_db=False, amax
     _ring_on(ring_u, dy, "ring_u")
     _scalar(amax, dy, "amax")
     _scalar(amax_u, dy, "amax_u")
-    dev = dy.device
     L = _LIB or lib()
-    dz = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-    du = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if u is not None else None
+    dz = torch.empty_like(dy, dtype=torch.uint8)
+    du = torch.empty_like(dy, dtype=torch.uint8) if u is not None else None
     db = dbu = ws = None
     wsb = 0
     if need_db:
-        db = torch.empty(cols, dtype=torch.float32, device=dev)
+        db = dy.new_empty(cols, dtype=torch.float32)
         if u is not None:
-            dbu = torch.empty(cols, dtype=torch.float32, device=dev)
+            dbu = dy.new_empty(cols, dtype=torch.float32)
         wsb = L.fp8_act_backward_workspace_bytes(rows, cols, 0 if u is None else 1)
         if wsb:
-            ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
+            ws = dy.new_empty(wsb, dtype=torch.uint8)
     a = CActBwdArgs(dy.data_ptr(), IN_DTYPE[dy.dtype], _ptr(z), _ptr(u), rows, cols, act, fmt, ring.c(),
                     ring_u.c() if ring_u is not None else _NO_RING, _ptr(amax), _ptr(amax_u), dz.data_ptr(), _ptr(du),
                     _ptr(db), _ptr(dbu), _ptr(ws), wsb)
