@@ -73,13 +73,19 @@ __device__ __forceinline__ void codes8(const float (&v)[8], int fmt, float s, ui
   }
 }
 
+template <int ACT>
+__device__ __forceinline__ void slopes8(float (&z)[8], float (&sl)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) act_slope_pair<ACT>(z[i], z[i + 1], sl[i], sl[i + 1]);
+}
+
 // dz (and du) of one vector: codes out, |.| into the amaxes, values into the
 // sums.  Lanes beyond the row's end hold dy = 0, hence dz = du = 0.
 template <int DT, bool kAligned, bool kGate, bool kDb>
 __device__ __forceinline__ void emit_grads(const ActBwdArgs& a, int64_t e, int c, int cols, const Grads<DT, kGate>& g,
                                            float s, float su, float& amax, float& amax_u, float (&sum)[8],
                                            float (&sum_u)[8]) {
-  float d[8], z[8], u[8], w[8];
+  float d[8], z[8], u[8], w[8], sl[8];
   unpack8<DT>(g.dy, d);
   if (a.z != nullptr) {
     unpack8<FP8_IN_BF16>(g.z, z);
@@ -87,21 +93,28 @@ __device__ __forceinline__ void emit_grads(const ActBwdArgs& a, int64_t e, int c
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = 0.0f;
   }
-  if constexpr (kGate) unpack8<FP8_IN_BF16>(g.u, u);
+  switch (a.act) {  // uniform; z becomes act(z)
+    case FP8_ACT_RELU: slopes8<FP8_ACT_RELU>(z, sl); break;
+    case FP8_ACT_GELU: slopes8<FP8_ACT_GELU>(z, sl); break;
+    case FP8_ACT_SILU: slopes8<FP8_ACT_SILU>(z, sl); break;
+    default: slopes8<FP8_ACT_NONE>(z, sl);
+  }
+  if constexpr (kGate) {
+    unpack8<FP8_IN_BF16>(g.u, u);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float value, slope;
-    act_value_slope(a.act, z[i], value, slope);
-    if constexpr (kGate) {
-      w[i] = d[i] * value;
-      d[i] = (d[i] * u[i]) * slope;
-      amax_u = fmaxf(amax_u, fabsf(w[i]));
-      if constexpr (kDb) sum_u[i] += w[i];
-    } else {
-      d[i] = d[i] * slope;
+    for (int i = 0; i < 8; i += 2) {
+      w[i] = d[i], w[i + 1] = d[i + 1];
+      mul2(w[i], w[i + 1], z[i], z[i + 1]);
+      mul2(d[i], d[i + 1], u[i], u[i + 1]);
     }
-    amax = fmaxf(amax, fabsf(d[i]));
-    if constexpr (kDb) sum[i] += d[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    mul2(d[i], d[i + 1], sl[i], sl[i + 1]);
+    amax = fmaxf(amax, fmaxf(fabsf(d[i]), fabsf(d[i + 1])));
+    if constexpr (kGate) amax_u = fmaxf(amax_u, fmaxf(fabsf(w[i]), fabsf(w[i + 1])));
+    if constexpr (kDb) add2(sum[i], sum[i + 1], d[i], d[i + 1]);
+    if constexpr (kDb && kGate) add2(sum_u[i], sum_u[i + 1], w[i], w[i + 1]);
   }
   uint32_t lo, hi;
   codes8(d, a.fmt, s, lo, hi);

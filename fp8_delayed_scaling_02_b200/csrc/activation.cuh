@@ -6,7 +6,7 @@
 //         w = 2 sqrt(2/pi) (z + 0.044715 z^3): the tanh form, since
 //         (1 + tanh(w/2)) / 2 is the logistic function of w
 //
-// p and q both come from t = e^-|w| in (0, 1]: r = 1/(1+t) is one of them and
+// logistic: p and q both come from t = e^-|w| in (0, 1]: r = 1/(1+t) is one of them and
 // t r the other, so neither cancels nor overflows, however large |w|.  The
 // fast exponential and division are within (2 + 1.2 |w|) and 2 float32 ulp
 // (CUDA's stated bounds): far inside what the 8- and 16-bit outputs keep.
@@ -40,31 +40,6 @@ __device__ __forceinline__ float act_value(int act, float z) {
     case FP8_ACT_SILU: logistic(z, p, q); return z * p;
     case FP8_ACT_GELU: logistic(z * fmaf(kGeluC2 * kGeluA, square_capped(z), kGeluC2), p, q); return z * p;
     default: return z;
-  }
-}
-
-__device__ __forceinline__ void act_value_slope(int act, float z, float& value, float& slope) {
-  float p, q;
-  switch (act) {
-    case FP8_ACT_RELU:
-      value = z < 0.0f ? 0.0f : z;
-      slope = z > 0.0f ? 1.0f : 0.0f;
-      return;
-    case FP8_ACT_SILU:
-      logistic(z, p, q);
-      value = z * p;
-      slope = fmaf(value, q, p);
-      return;
-    case FP8_ACT_GELU: {
-      const float s = square_capped(z);
-      logistic(z * fmaf(kGeluC2 * kGeluA, s, kGeluC2), p, q);
-      value = z * p;
-      slope = fmaf(value * q, fmaf(3.0f * kGeluC2 * kGeluA, s, kGeluC2), p);
-      return;
-    }
-    default:
-      value = z;
-      slope = 1.0f;
   }
 }
 
@@ -133,6 +108,53 @@ __device__ __forceinline__ void act_pair(float& a, float& b) {
     y = exp2_fast(y);
     add2(x, y, 1.0f, 1.0f);
     mul2(a, b, rcp_fast(x), rcp_fast(y));
+  }
+}
+
+// value and slope of a pair: q = 1 - p is off by at most 2^-24, which the slope
+// p + z p q multiplies by |z p|.  z^2 is capped so that p q = 0 times it is 0.
+__device__ __forceinline__ void fma2v(float& a, float& b, float c, float d, float e, float f) {  // (a c + e, b d + f)
+  asm("{\n\t.reg .b64 ra, rc, re;\n\t"
+      "mov.b64 ra, {%0, %1};\n\t"
+      "mov.b64 rc, {%2, %3};\n\t"
+      "mov.b64 re, {%4, %5};\n\t"
+      "fma.rn.f32x2 ra, ra, rc, re;\n\t"
+      "mov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d), "f"(e), "f"(f));
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_slope_pair(float& a, float& b, float& sa, float& sb) {
+  if constexpr (ACT == FP8_ACT_NONE) {
+    sa = sb = 1.0f;
+  } else if constexpr (ACT == FP8_ACT_RELU) {
+    sa = a > 0.0f ? 1.0f : 0.0f;
+    sb = b > 0.0f ? 1.0f : 0.0f;
+    a = max_nan(a, 0.0f);
+    b = max_nan(b, 0.0f);
+  } else {
+    float x = a, y = b, wx = 1.0f, wy = 1.0f;  // e^-w; w'
+    if constexpr (ACT == FP8_ACT_GELU) {
+      constexpr float c1 = -kGeluC2 * kLog2E;
+      const float s = square_capped(a), t = square_capped(b);
+      x = s, y = t;
+      fma2(x, y, c1 * kGeluA, c1, c1);
+      mul2(x, y, a, b);
+      wx = s, wy = t;
+      fma2(wx, wy, 3.0f * kGeluC2 * kGeluA, kGeluC2, kGeluC2);
+    } else {
+      scale2(x, y, -kLog2E);
+    }
+    x = exp2_fast(x);
+    y = exp2_fast(y);
+    add2(x, y, 1.0f, 1.0f);
+    const float p = rcp_fast(x), r = rcp_fast(y);
+    mul2(a, b, p, r);
+    sa = p, sb = r;
+    fma2(sa, sb, -1.0f, 1.0f, 1.0f);  // q
+    if constexpr (ACT == FP8_ACT_GELU) mul2(sa, sb, wx, wy);
+    fma2v(sa, sb, a, b, p, r);
   }
 }
 

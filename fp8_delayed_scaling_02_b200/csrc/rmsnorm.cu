@@ -5,15 +5,17 @@
 // Both are streams bound by HBM: forward 2 reads, 1 write and 1 code byte per
 // element with a residual, backward 3 reads and 1 write.  So each element is
 // read once and stays in registers, packed as it lies in memory:
-//   * a group of W warps (1, 2, 4, 8 or 16) owns a row, each thread V <= 4
-//     vectors of 8 elements at fixed columns; gamma for those columns is read
-//     once per thread and kept, and so are the partial sums of dgamma;
+//   * a group of W warps owns a row, each thread V vectors of 8 elements at
+//     fixed columns (W = 6, V = 1 for 1536 columns: no idle lanes); the next
+//     row's loads go out before the row in work is reduced;
 //   * the row's statistics cross lanes by shuffles and, where W > 1, warps by
 //     one shared word each and a named barrier of the group alone;
+//   * gamma comes from L1 for each row, its load ahead of the reduction: kept
+//     in registers it costs the occupancy that keeps the loads in flight;
 //   * groups walk over the rows of one wave of resident blocks;
-//   * dgamma: each block adds its groups' partial sums in order and writes one
-//     float32 row; a second launch adds those rows, in order, so every bit
-//     depends on the sizes and the device only.
+//   * dgamma: partial sums per thread, then each block adds its groups' in
+//     order and writes one float32 row; a second launch adds those rows, in
+//     order, so every bit depends on the sizes and the device only.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -32,7 +34,8 @@ namespace fp8ds {
 namespace {
 
 constexpr int kMaxCols = 16384;  // 16 warps x 32 lanes x 4 vectors x 8
-constexpr int kMaxVec = 4;
+constexpr int kMaxWarps = 16;    // per row
+constexpr int kRedWords = 24;    // warps of a block, at most
 
 struct NormArgs {
   const uint8_t* x;
@@ -42,7 +45,7 @@ struct NormArgs {
   float eps;
   int64_t rows;
   int cols;
-  int log_w;         // warps per row, log2
+  int warps, groups; // warps per row, rows in work per block
   uint8_t* h;
   uint8_t* y;
   float* rstd;
@@ -62,7 +65,7 @@ struct NormBwdArgs {
   int gamma_f32;
   int64_t rows;
   int cols;
-  int log_w;
+  int warps, groups;
   uint8_t* dx;
   float* partial;    // [gridDim.x][cols] sums of dy * n, or null
 };
@@ -71,9 +74,8 @@ struct NormBwdArgs {
 // group calls it; the result is the same in all of them.  The two halves of
 // `sm` alternate between calls: a warp can write a half again only after a
 // barrier that every reader of its last contents has reached.
-template <int NT>
 struct GroupReduce {
-  float* sm;  // [2][NT / 32]
+  float* sm;  // [2][kRedWords]
   int warps, group, warp_in_group, flip;
 
   template <typename Op>
@@ -81,7 +83,7 @@ struct GroupReduce {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     if (warps == 1) return v;
-    float* buf = sm + flip * (NT / 32) + group * warps;
+    float* buf = sm + flip * kRedWords + group * warps;
     if ((threadIdx.x & 31) == 0) buf[warp_in_group] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * warps) : "memory");
     float r = buf[0];
@@ -97,66 +99,83 @@ struct GroupReduce {
   }
 };
 
-template <int DT>
+// Eight values of gamma (kAligned: gamma too is 16-byte aligned).
+template <int DT, bool kAligned>
 __device__ __forceinline__ void load_gamma8(const void* gamma, int f32, int c, int cols, float (&g)[8]) {
   const uint8_t* p = static_cast<const uint8_t*>(gamma);
-  if (f32) unpack8<FP8_IN_FP32>(load8<FP8_IN_FP32, false>(p, c, cols), g);
-  else unpack8<DT>(load8<DT, false>(p, c, cols), g);
+  if (f32) unpack8<FP8_IN_FP32>(load8<FP8_IN_FP32, kAligned>(p, c, cols), g);
+  else unpack8<DT>(load8<DT, kAligned>(p, c, cols), g);
 }
 
 template <int DT, bool kAligned, int V, int NT>
 __global__ void __launch_bounds__(NT) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   constexpr int kB = In<DT>::kBytes;
-  __shared__ float red[2 * (NT / 32)];
+  // Up to two vectors per thread: the next row's loads go out ahead of the row
+  // in work, and gamma is read again for each row.  Four: gamma is kept instead.
+  constexpr bool kAhead = V <= 2;
+  __shared__ float red[2 * kRedWords];
+  __shared__ float hist_s[kHistoryLen];
+  __shared__ int idx_s;
   pdl_launch_dependents();
   pdl_wait_prior_grid();
-  const int warps = 1 << a.log_w;
-  const int warp = threadIdx.x >> 5;
-  const int group = warp >> a.log_w;
-  const int groups = (NT / 32) >> a.log_w;
-  const int t = threadIdx.x - ((group << a.log_w) << 5);
-  const int stride = 256 << a.log_w;  // columns between a thread's vectors
-  GroupReduce<NT> gr{red, warps, group, warp - (group << a.log_w), 0};
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = warp / a.warps;
+  const int t = threadIdx.x - group * a.warps * 32;
+  const int stride = 256 * a.warps;  // columns between a thread's vectors
+  GroupReduce gr{red, a.warps, group, warp - group * a.warps, 0};
 
-  const bool ring_mode = a.fold != 0;
-  const float s_ring = ring_mode ? *a.ring.scale : 1.0f;
-  RingCache rc{0.0f, 0};
-  if (ring_mode) rc = prefetch_ring(a.ring);
-  float gm[V][8];
-#pragma unroll
-  for (int v = 0; v < V; ++v) load_gamma8<DT>(a.gamma, a.gamma_f32, 8 * t + v * stride, a.cols, gm[v]);
-
+  const float s_ring = a.fold ? *a.ring.scale : 1.0f;
+  if (a.fold && a.ring.amax_out == nullptr) {  // not written before the last block's fold
+    if (threadIdx.x < kHistoryLen) hist_s[threadIdx.x] = a.ring.history[threadIdx.x];
+    if (threadIdx.x == kHistoryLen) idx_s = *a.ring.idx;
+  }
   const float inv_cols = __frcp_rn(float(a.cols));
   const float fmax = a.fmt == FP8_E5M2 ? kE5M2Max : kE4M3Max;
+  const int64_t step = int64_t(gridDim.x) * a.groups;
   float amax = 0.0f;
-  for (int64_t row = int64_t(blockIdx.x) * groups + group; row < a.rows; row += int64_t(gridDim.x) * groups) {
+  Vec8<DT> nx[V], nr[V];  // the next row of x and residual
+  auto load = [&](int64_t row) {
+    const int64_t off = row * a.cols * kB;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      nx[v] = load8<DT, kAligned>(a.x + off, 8 * t + v * stride, a.cols);
+      if (a.res != nullptr) nr[v] = load8<DT, kAligned>(a.res + off, 8 * t + v * stride, a.cols);
+    }
+  };
+  float gm[V][8];
+  auto load_gamma = [&]() {
+#pragma unroll
+    for (int v = 0; v < V; ++v) load_gamma8<DT, kAligned>(a.gamma, a.gamma_f32, 8 * t + v * stride, a.cols, gm[v]);
+  };
+  if (!kAhead) load_gamma();
+  int64_t row = int64_t(blockIdx.x) * a.groups + group;
+  if (row < a.rows) load(row);
+  for (; row < a.rows; row += step) {
     const int64_t off = row * a.cols * kB;
     Vec8<DT> h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = load8<DT, kAligned>(a.x + off, 8 * t + v * stride, a.cols);
-    if (a.res != nullptr) {
-      Vec8<DT> r[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) r[v] = load8<DT, kAligned>(a.res + off, 8 * t + v * stride, a.cols);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float p[8], q[8];
-        unpack8<DT>(h[v], p);
-        unpack8<DT>(r[v], q);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] += q[i];
-        h[v] = pack8<DT>(p);
-        store8<DT, kAligned>(a.h + off, 8 * t + v * stride, a.cols, h[v]);
-      }
-    }
     float ss = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float p[8];
-      unpack8<DT>(h[v], p);
+      unpack8<DT>(nx[v], p);
+      h[v] = nx[v];
+      if (a.res != nullptr) {
+        float q[8];
+        unpack8<DT>(nr[v], q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] += q[i];
+        h[v] = pack8<DT>(p);
+        unpack8<DT>(h[v], p);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(p[i], p[i], ss);
     }
+    if (kAhead && row + step < a.rows) load(row + step);
+    if (a.res != nullptr) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) store8<DT, kAligned>(a.h + off, 8 * t + v * stride, a.cols, h[v]);
+    }
+    if (kAhead) load_gamma();
     const float rstd = rsqrtf(fmaf(gr.sum(ss), inv_cols, a.eps));
     if (a.rstd != nullptr && t == 0) a.rstd[row] = rstd;
     float s = s_ring;
@@ -200,50 +219,66 @@ __global__ void __launch_bounds__(NT) rmsnorm_kernel(const __grid_constant__ Nor
         store8_codes<kAligned>(a.codes + row * a.cols, c, a.cols, lo, hi);
       }
     }
+    if (!kAhead && row + step < a.rows) load(row + step);
   }
-  if (ring_mode) {
-    if (a.fmt == FP8_E5M2) amax_ticket_fold<FP8_E5M2, NT>(amax, a.ring, s_ring, rc, gridDim.x);
-    else amax_ticket_fold<FP8_E4M3, NT>(amax, a.ring, s_ring, rc, gridDim.x);
-  }
+  if (!a.fold) return;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  __syncthreads();  // every group is done with `red`
+  if (lane == 0) red[warp] = amax;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < a.warps * a.groups; ++w) amax = fmaxf(amax, red[w]);
+  if (a.fmt == FP8_E5M2) commit_block_amax<FP8_E5M2>(amax, a.ring, s_ring, hist_s, idx_s, gridDim.x);
+  else commit_block_amax<FP8_E4M3>(amax, a.ring, s_ring, hist_s, idx_s, gridDim.x);
 }
 
 template <int DT, bool kAligned, int V, int NT>
 __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
   constexpr int kB = In<DT>::kBytes;
-  // Rows of up to 1024 V columns (four warps or fewer) share a block with
-  // other groups, whose dgamma sums are added here.
-  __shared__ float red[2 * (NT / 32)];
-  __shared__ float sum_s[NT == 256 ? 1024 * V : 1];
+  constexpr bool kAhead = V * kB <= 4;  // the next row's loads go out early, as far as the registers last
+  __shared__ float red[2 * kRedWords];
+  extern __shared__ float sum_s[];  // [cols], where several groups' dgamma sums meet
   pdl_launch_dependents();
   pdl_wait_prior_grid();
-  const int warps = 1 << a.log_w;
   const int warp = threadIdx.x >> 5;
-  const int group = warp >> a.log_w;
-  const int groups = (NT / 32) >> a.log_w;
-  const int t = threadIdx.x - ((group << a.log_w) << 5);
-  const int stride = 256 << a.log_w;
-  GroupReduce<NT> gr{red, warps, group, warp - (group << a.log_w), 0};
-  float gm[V][8], dg[V][8];
+  const int group = warp / a.warps;
+  const int t = threadIdx.x - group * a.warps * 32;
+  const int stride = 256 * a.warps;
+  GroupReduce gr{red, a.warps, group, warp - group * a.warps, 0};
+  float dg[V][8];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    load_gamma8<DT>(a.gamma, a.gamma_f32, 8 * t + v * stride, a.cols, gm[v]);
+  for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dg[v][i] = 0.0f;
-  }
   const float inv_cols = __frcp_rn(float(a.cols));
-  for (int64_t row = int64_t(blockIdx.x) * groups + group; row < a.rows; row += int64_t(gridDim.x) * groups) {
+  const int64_t step = int64_t(gridDim.x) * a.groups;
+  Vec8<DT> ny[V], nh[V], nr[V];  // the next row of dy, h and dres
+  float nrstd = 0.0f;
+  auto load = [&](int64_t row) {
     const int64_t off = row * a.cols * kB;
-    const float rstd = a.rstd[row];
-    Vec8<DT> dy[V], h[V], dr[V];
+    nrstd = a.rstd[row];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      dy[v] = load8<DT, kAligned>(a.dy + off, 8 * t + v * stride, a.cols);
-      h[v] = load8<DT, kAligned>(a.h + off, 8 * t + v * stride, a.cols);
-      if (a.dres != nullptr) dr[v] = load8<DT, kAligned>(a.dres + off, 8 * t + v * stride, a.cols);
+      ny[v] = load8<DT, kAligned>(a.dy + off, 8 * t + v * stride, a.cols);
+      nh[v] = load8<DT, kAligned>(a.h + off, 8 * t + v * stride, a.cols);
+      if (a.dres != nullptr) nr[v] = load8<DT, kAligned>(a.dres + off, 8 * t + v * stride, a.cols);
     }
+  };
+  int64_t row = int64_t(blockIdx.x) * a.groups + group;
+  if (row < a.rows) load(row);
+  for (; row < a.rows; row += step) {
+    const int64_t off = row * a.cols * kB;
+    const float rstd = nrstd;
+    Vec8<DT> dy[V], h[V], dr[V];
+    float gm[V][8];
     float dot = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      load_gamma8<DT, kAligned>(a.gamma, a.gamma_f32, 8 * t + v * stride, a.cols, gm[v]);
+      dy[v] = ny[v];
+      h[v] = nh[v];
+      dr[v] = nr[v];
       float d[8], n[8];
       unpack8<DT>(dy[v], d);
       unpack8<DT>(h[v], n);
@@ -254,6 +289,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(const __grid_constant__
         dot = fmaf(e, gm[v][i], dot);
       }
     }
+    if (kAhead && row + step < a.rows) load(row + step);
     const float c1 = gr.sum(dot) * inv_cols;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -270,25 +306,26 @@ __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(const __grid_constant__
       for (int i = 0; i < 8; ++i) e[i] = fmaf(rstd, fmaf(-(n[i] * rstd), c1, d[i] * gm[v][i]), e[i]);
       store8<DT, kAligned>(a.dx + off, 8 * t + v * stride, a.cols, pack8<DT>(e));
     }
+    if (!kAhead && row + step < a.rows) load(row + step);
   }
   if (a.partial == nullptr) return;
   float* out = a.partial + int64_t(blockIdx.x) * a.cols;
-  if (groups > 1) {
-    for (int g = 0; g < groups; ++g) {
-      if (group == g) {
+  if (a.groups > 1) {
+    for (int q = 0; q < a.groups; ++q) {
+      if (group == q) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int c = 8 * t + v * stride;
+        for (int v = 0; v < V; ++v)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if (g > 0) dg[v][i] += sum_s[c + i];
-            sum_s[c + i] = dg[v][i];
+            const int c = 8 * t + v * stride + i;
+            if (c >= a.cols) continue;
+            if (q > 0) dg[v][i] += sum_s[c];
+            sum_s[c] = dg[v][i];
           }
-        }
       }
       __syncthreads();
     }
-    if (group != groups - 1) return;
+    if (group != a.groups - 1) return;
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -301,26 +338,38 @@ __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(const __grid_constant__
 
 // ---- host side -----------------------------------------------------------------
 
-// How a row is split: W = 2^log_w warps and V vectors per thread.
+// How a row is split: `warps` warps of threads with v vectors each, and how
+// many rows a block has in work.
 struct RowSplit {
-  int log_w, v, nt;
+  int warps, groups, v;
+  int threads() const { return 32 * warps * groups; }
 };
 
-RowSplit split_row(int64_t rows, int64_t cols) {
-  const int64_t vecs = (cols + 7) / 8;
-  RowSplit s{0, 1, 256};
-  while ((vecs + (32 << s.log_w) - 1) / (32 << s.log_w) > kMaxVec) ++s.log_w;
-  // Few rows: more warps on each, so that a row's loads are in flight at once.
-  while (s.log_w < 3 && vecs > (32 << s.log_w) && (rows << s.log_w) < 148 * 8) ++s.log_w;
-  s.v = int((vecs + (32 << s.log_w) - 1) / (32 << s.log_w));
-  s.nt = s.log_w > 3 ? 512 : 256;
+RowSplit split_at(int64_t cols, int v, int block_warps) {
+  RowSplit s;
+  s.v = v;
+  s.warps = int(((cols + 7) / 8 + 32 * v - 1) / (32 * v));
+  s.groups = std::max(1, block_warps / s.warps);
   return s;
 }
 
-int64_t bwd_blocks(int64_t rows, int64_t cols, int sms) {
-  const RowSplit s = split_row(rows, cols);
-  const int64_t groups = (s.nt / 32) >> s.log_w;
-  return std::max<int64_t>(1, std::min<int64_t>((rows + groups - 1) / groups, 2 * int64_t(sms)));
+// Forward: two vectors per thread (one for a row that fits one warp, four
+// above 4096 columns of 16 bits, 8192 of 32), blocks of about eight warps.  8192 x 1536 bf16 with a
+// residual, by vectors per thread: one 25.8 us (six warps meet at each row's
+// barrier), two 16.9, three 21.2, four 23.7; without the next row's loads
+// ahead, two take 20.2.  4096 x 8192: two (sixteen warps) 52.6 us, four 45.9.
+RowSplit split_fwd(int64_t cols, int bytes) {
+  return split_at(cols, cols <= 256 ? 1 : cols <= (bytes == 4 ? 8192 : 4096) ? 2 : 4, 8);
+}
+
+// Backward: one vector per thread while a row's warps fit a block, for the
+// dgamma sums and the second pass need the registers, and one large block per
+// SM, so that there are few rows of partial sums.
+constexpr int bwd_threads(int bytes, bool aligned, int v) { return bytes == 2 && aligned && v == 1 ? 768 : 512; }
+
+RowSplit split_bwd(int64_t cols, int bytes, bool aligned) {
+  const int v = cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4;
+  return split_at(cols, v, bwd_threads(bytes, aligned, v) / 32);
 }
 
 int norm_shape_check(int dtype, int64_t rows, int64_t cols) {
@@ -330,50 +379,49 @@ int norm_shape_check(int dtype, int64_t rows, int64_t cols) {
   return FP8_OK;
 }
 
-template <typename K, typename A>
-int launch_rows(K kern, const A& a, int64_t rows, const RowSplit& s, int64_t most, int (&cached)[64],
-                cudaStream_t st) {
-  const int bps = resident_blocks(kern, s.nt, cached);
-  const int sms = sm_count_current();
-  if (bps < 1 || sms < 1) return FP8_ERR_CUDA;
-  const int64_t groups = (s.nt / 32) >> s.log_w;
-  int64_t grid = std::max<int64_t>(1, std::min<int64_t>((rows + groups - 1) / groups, int64_t(sms) * bps));
-  if (most > 0) grid = most;
-  return launch_pdl(kern, dim3(unsigned(grid)), dim3(s.nt), 0, st, 1, a) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
-}
-
 template <int DT, bool kAligned, int V, int NT>
 int launch_fwd1(const NormArgs& a, const RowSplit& s, cudaStream_t st) {
-  static int cached[64] = {0};
-  return launch_rows(rmsnorm_kernel<DT, kAligned, V, NT>, a, a.rows, s, 0, cached, st);
+  static int cached[64][kMaxWarps + 1] = {{0}};  // resident blocks per SM by warps per row
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8_ERR_CUDA;
+  int& bps = cached[dev][s.warps];
+  if (bps == 0) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, rmsnorm_kernel<DT, kAligned, V, NT>, s.threads(), 0) !=
+            cudaSuccess || n < 1)
+      return FP8_ERR_CUDA;
+    bps = n;
+  }
+  const int sms = sm_count_current();
+  if (sms < 1) return FP8_ERR_CUDA;
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((a.rows + s.groups - 1) / s.groups, int64_t(sms) * bps));
+  return launch_pdl(rmsnorm_kernel<DT, kAligned, V, NT>, dim3(unsigned(grid)), dim3(s.threads()), 0, st, 1, a) ==
+                 cudaSuccess
+             ? FP8_OK
+             : FP8_ERR_CUDA;
 }
 
 template <int DT, bool kAligned>
 int launch_fwd(const NormArgs& a, const RowSplit& s, cudaStream_t st) {
-  if (s.nt == 512) return s.v <= 3 ? launch_fwd1<DT, kAligned, 3, 512>(a, s, st) : launch_fwd1<DT, kAligned, 4, 512>(a, s, st);
-  switch (s.v) {
-    case 1: return launch_fwd1<DT, kAligned, 1, 256>(a, s, st);
-    case 2: return launch_fwd1<DT, kAligned, 2, 256>(a, s, st);
-    case 3: return launch_fwd1<DT, kAligned, 3, 256>(a, s, st);
-    default: return launch_fwd1<DT, kAligned, 4, 256>(a, s, st);
-  }
+  if (s.v == 4) return launch_fwd1<DT, kAligned, 4, 512>(a, s, st);
+  if (s.v == 2) return launch_fwd1<DT, kAligned, 2, 512>(a, s, st);
+  return launch_fwd1<DT, kAligned, 1, 256>(a, s, st);
 }
 
-template <int DT, bool kAligned, int V, int NT>
+template <int DT, bool kAligned, int V>
 int launch_bwd1(const NormBwdArgs& a, const RowSplit& s, int64_t grid, cudaStream_t st) {
-  static int cached[64] = {0};
-  return launch_rows(rmsnorm_bwd_kernel<DT, kAligned, V, NT>, a, a.rows, s, grid, cached, st);
+  // Shared sums of several groups: at most 8192 columns, since more leave one group.
+  const size_t smem = s.groups > 1 ? size_t(a.cols) * 4 : 0;
+  const cudaError_t e = launch_pdl(rmsnorm_bwd_kernel<DT, kAligned, V, bwd_threads(In<DT>::kBytes, kAligned, V)>,
+                                   dim3(unsigned(grid)), dim3(s.threads()), smem, st, 1, a);
+  return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
 template <int DT, bool kAligned>
-int launch_bwd(const NormBwdArgs& a, const RowSplit& s, int64_t g, cudaStream_t st) {
-  if (s.nt == 512) return s.v <= 3 ? launch_bwd1<DT, kAligned, 3, 512>(a, s, g, st) : launch_bwd1<DT, kAligned, 4, 512>(a, s, g, st);
-  switch (s.v) {
-    case 1: return launch_bwd1<DT, kAligned, 1, 256>(a, s, g, st);
-    case 2: return launch_bwd1<DT, kAligned, 2, 256>(a, s, g, st);
-    case 3: return launch_bwd1<DT, kAligned, 3, 256>(a, s, g, st);
-    default: return launch_bwd1<DT, kAligned, 4, 256>(a, s, g, st);
-  }
+int launch_bwd(const NormBwdArgs& a, const RowSplit& s, int64_t grid, cudaStream_t st) {
+  if (s.v == 4) return launch_bwd1<DT, kAligned, 4>(a, s, grid, st);
+  if (s.v == 2) return launch_bwd1<DT, kAligned, 2>(a, s, grid, st);
+  return launch_bwd1<DT, kAligned, 1>(a, s, grid, st);
 }
 
 }  // namespace
@@ -434,10 +482,11 @@ extern "C" int fp8_rmsnorm(const fp8_rmsnorm_args* p, fp8_stream_t stream) {
   a.row_sinv = p->row_sinv;
   if (ring_mode)
     a.ring = RingArgs{p->ring.history, p->ring.idx, p->ring.scale, p->ring.scale_inv, p->ring.scratch, p->amax_out};
-  const RowSplit s = split_row(p->rows, p->cols);
-  a.log_w = s.log_w;
+  const RowSplit s = split_fwd(p->cols, eb);
+  a.warps = s.warps;
+  a.groups = s.groups;
   const bool al = p->cols % 8 == 0 && on(p->x, 16) && on(p->residual, 16) && on(p->h, 16) && on(p->y, 16) &&
-                  on(p->codes, 8);
+                  on(p->codes, 8) && on(p->gamma, 16);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   switch (p->dtype) {
     case FP8_IN_BF16: return al ? launch_fwd<FP8_IN_BF16, true>(a, s, st) : launch_fwd<FP8_IN_BF16, false>(a, s, st);
@@ -450,7 +499,7 @@ extern "C" size_t fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t col
   if (rows <= 0 || cols <= 0 || cols > kMaxCols || rows > INT32_MAX) return 0;
   const int sms = sm_count_current();
   if (sms <= 0) return 0;
-  const int64_t n = bwd_blocks(rows, cols, sms);
+  const int64_t n = std::min<int64_t>(rows, sms);  // blocks, at most
   return n > 1 ? size_t(n) * size_t(cols) * 4 : 0;
 }
 
@@ -480,8 +529,11 @@ extern "C" int fp8_rmsnorm_backward(const fp8_rmsnorm_backward_args* p, fp8_stre
   if (p->rows == 0 && p->dgamma == nullptr) return FP8_OK;
   const int sms = sm_count_current();
   if (sms <= 0) return FP8_ERR_CUDA;
-  const RowSplit s = split_row(p->rows, p->cols);
-  const int64_t grid = bwd_blocks(p->rows, p->cols, sms);
+  const bool al = p->cols % 8 == 0 && on(p->dy, 16) && on(p->h, 16) && on(p->dres, 16) && on(p->dx, 16) &&
+                  on(p->gamma, 16);
+  RowSplit s = split_bwd(p->cols, eb, al);
+  s.groups = int(std::max<int64_t>(1, std::min<int64_t>(s.groups, (p->rows + sms - 1) / sms)));  // few rows: all SMs
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((p->rows + s.groups - 1) / s.groups, sms));
   NormBwdArgs a{};
   a.dy = static_cast<const uint8_t*>(p->dy);
   a.h = static_cast<const uint8_t*>(p->h);
@@ -491,7 +543,8 @@ extern "C" int fp8_rmsnorm_backward(const fp8_rmsnorm_backward_args* p, fp8_stre
   a.gamma_f32 = p->gamma_f32 != 0 || p->dtype == FP8_IN_FP32;
   a.rows = p->rows;
   a.cols = int(p->cols);
-  a.log_w = s.log_w;
+  a.warps = s.warps;
+  a.groups = s.groups;
   a.dx = static_cast<uint8_t*>(p->dx);
   if (p->rows == 0) {  // no rows: the empty sum
     return launch_colsum(nullptr, 0, p->cols, p->dgamma, st);
@@ -504,7 +557,6 @@ extern "C" int fp8_rmsnorm_backward(const fp8_rmsnorm_backward_args* p, fp8_stre
       a.partial = p->dgamma;  // one block: its sums are the result
     }
   }
-  const bool al = p->cols % 8 == 0 && on(p->dy, 16) && on(p->h, 16) && on(p->dres, 16) && on(p->dx, 16);
   int r;
   switch (p->dtype) {
     case FP8_IN_BF16: r = al ? launch_bwd<FP8_IN_BF16, true>(a, s, grid, st) : launch_bwd<FP8_IN_BF16, false>(a, s, grid, st); break;
