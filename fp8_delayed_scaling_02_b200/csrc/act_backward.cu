@@ -7,9 +7,8 @@
 // into its own ring by the last block) and, where wanted, the column sums.
 //   * Without sums the tensors are one flat run of 8-element vectors, two in
 //     flight per thread, over one wave of resident blocks.
-//   * With sums a block owns a strip of 64 columns (whole 128-byte lines of
-//     bf16) and walks down its rows 32 at a time, so a thread's 8 columns stay
-//     fixed and their sums in registers; strips are cut into row chunks to
+//   * With sums a block owns a strip of 256 columns (or 64) and walks down its
+//     rows, so a thread's 8 columns stay fixed and their sums in registers; strips are cut into row chunks to
 //     fill one wave, each chunk writes one float32 row of partial sums, and a
 //     second launch adds those in order.
 #include <cuda_bf16.h>
@@ -31,8 +30,9 @@ namespace fp8ds {
 namespace {
 
 constexpr int kAbThreads = 256;
-constexpr int kStripCols = 64;                            // 8 lanes x 8 columns
-constexpr int kStripRows = kAbThreads / (kStripCols / 8);  // rows of one step of a block
+constexpr int kMaxStripCols = 256;
+// Blocks per SM of the kernels with sums, and so the registers they may use.
+constexpr int sum_blocks(bool gate) { return gate ? 3 : 4; }
 
 struct ActBwdArgs {
   const uint8_t* dy;
@@ -44,6 +44,7 @@ struct ActBwdArgs {
   uint8_t* dzq;
   uint8_t* duq;
   int64_t strips;    // with sums: blockIdx.x = chunk * strips + strip
+  int lanes;         // threads across a strip, 8 columns each: 8 or 32
   int64_t chunks;
   float* part;       // [chunks][cols] sums of dz
   float* part_u;     // and of du
@@ -134,11 +135,11 @@ __device__ __forceinline__ void commit_ring(const ActBwdArgs& a, const RingArgs&
 }
 
 template <int DT, bool kAligned, bool kGate, bool kDb>
-__global__ void __launch_bounds__(kAbThreads) act_backward_kernel(const __grid_constant__ ActBwdArgs a) {
+__global__ void __launch_bounds__(kAbThreads, kDb ? sum_blocks(kGate) : 3) act_backward_kernel(const __grid_constant__ ActBwdArgs a) {
   __shared__ float warp_max[2][kAbThreads / 32];
   __shared__ float hist_s[2][kHistoryLen];
   __shared__ int idx_s[2];
-  __shared__ float sum_s[kDb ? 2 * (kAbThreads / 32) * kStripCols : 1];
+  __shared__ float sum_s[kDb ? (kGate ? 2 : 1) * (kAbThreads / 32) * kMaxStripCols : 1];
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -160,30 +161,29 @@ __global__ void __launch_bounds__(kAbThreads) act_backward_kernel(const __grid_c
   if constexpr (kDb) {
     const int64_t chunk = blockIdx.x / a.strips, strip = blockIdx.x - chunk * a.strips;
     const int cols = int(a.cols);
-    const int c = int(strip * kStripCols) + 8 * (threadIdx.x & 7);
-    const int64_t step = a.chunks * kStripRows;
-    for (int64_t r = chunk * kStripRows + (threadIdx.x >> 3); r < a.rows; r += 2 * step) {
+    const int c = int(strip) * 8 * a.lanes + 8 * (threadIdx.x & (a.lanes - 1));
+    const int rows = kAbThreads / a.lanes;  // of one step of a block
+    const int64_t step = a.chunks * rows;
+    for (int64_t r = chunk * rows + threadIdx.x / a.lanes; r < a.rows; r += 2 * step) {
       const bool two = r + step < a.rows;
       load_grads<DT, kAligned>(a, r * a.cols, c, cols, g0);
       if (two) load_grads<DT, kAligned>(a, (r + step) * a.cols, c, cols, g1);
       emit_grads<DT, kAligned, kGate, kDb>(a, r * a.cols, c, cols, g0, s, su, amax, amax_u, sum, sum_u);
       if (two) emit_grads<DT, kAligned, kGate, kDb>(a, (r + step) * a.cols, c, cols, g1, s, su, amax, amax_u, sum, sum_u);
     }
-    // 4 rows of a warp by shuffles, 8 warps through shared memory, in order.
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 8);
-      sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 16);
-      if constexpr (kGate) {
-        sum_u[i] += __shfl_xor_sync(0xFFFFFFFFu, sum_u[i], 8);
-        sum_u[i] += __shfl_xor_sync(0xFFFFFFFFu, sum_u[i], 16);
-      }
-    }
-    if (lane < 8) {
+    // A warp's rows by shuffles (narrow strips), the warps through shared memory, in order.
+    for (int o = a.lanes; o < 32; o <<= 1) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sum_s[warp * kStripCols + 8 * lane + i] = sum[i];
-        if constexpr (kGate) sum_s[(kAbThreads / 32 + warp) * kStripCols + 8 * lane + i] = sum_u[i];
+        sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
+        if constexpr (kGate) sum_u[i] += __shfl_xor_sync(0xFFFFFFFFu, sum_u[i], o);
+      }
+    }
+    if (lane < a.lanes) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum_s[warp * kMaxStripCols + 8 * lane + i] = sum[i];
+        if constexpr (kGate) sum_s[(kAbThreads / 32 + warp) * kMaxStripCols + 8 * lane + i] = sum_u[i];
       }
     }
   } else {
@@ -217,28 +217,47 @@ __global__ void __launch_bounds__(kAbThreads) act_backward_kernel(const __grid_c
   }
   if constexpr (kDb) {
     const int64_t chunk = blockIdx.x / a.strips, strip = blockIdx.x - chunk * a.strips;
-    const int which = threadIdx.x / kStripCols, col = threadIdx.x % kStripCols;
-    float* out = which == 0 ? a.part : which == 1 ? a.part_u : nullptr;
-    const int64_t c = strip * kStripCols + col;
-    if (out != nullptr && which < (kGate ? 2 : 1) && c < a.cols) {
-      float r = 0.0f;
+    const int width = 8 * a.lanes;
+    const int64_t c = strip * width + threadIdx.x;
+    if (threadIdx.x < width && c < a.cols) {
 #pragma unroll
-      for (int w = 0; w < kAbThreads / 32; ++w) r += sum_s[(which * (kAbThreads / 32) + w) * kStripCols + col];
-      out[chunk * a.cols + c] = r;
+      for (int k = 0; k < (kGate ? 2 : 1); ++k) {
+        float* out = k == 0 ? a.part : a.part_u;
+        if (out == nullptr) continue;
+        float r = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAbThreads / 32; ++w) r += sum_s[(k * (kAbThreads / 32) + w) * kMaxStripCols + threadIdx.x];
+        out[chunk * a.cols + c] = r;
+      }
     }
   }
 }
 
 // ---- host side -----------------------------------------------------------------
 
-constexpr int kSumBlocksPerSm = 4;  // blocks of 256 threads that the grid with sums counts on
+// Threads across a strip and row chunks per strip.
+//   * Up to kFewRows rows: narrow strips of one chunk, whose sums are the
+//     result (128 x 4096 gated: 6.9 us, in two launches 8.7).
+//   * More: as many chunks as fit in one wave together, of at least two steps
+//     each.  With a gate strips are as wide as a warp, unless that wastes over a
+//     sixteenth of the strips' columns (1537 columns: 7 strips of 256 for 6, 25
+//     of 64 for 24): 8192 x 4096 takes 53.6 us, in strips of 64 columns 65.9.
+//     Without, the fewer rows of partial sums of narrow strips count for more:
+//     512 x 4096 6.7 us, in strips of 256 7.6; 8192 x 1536 18.4 and 19.1.
+constexpr int64_t kFewRows = 256;
 
-int64_t strips_of(int64_t cols) { return (cols + kStripCols - 1) / kStripCols; }
+int lanes_of(int64_t rows, int64_t cols, bool gate) {
+  const int64_t wide = (cols + 255) / 256 * 256;
+  return gate && rows > kFewRows && wide - cols <= cols / 16 ? 32 : 8;
+}
 
-// Row chunks per strip: as many as fit in one wave together.
-int64_t chunks_of(int64_t rows, int64_t cols, int sms) {
-  const int64_t fit = int64_t(sms) * kSumBlocksPerSm / std::max<int64_t>(1, strips_of(cols));
-  return std::max<int64_t>(1, std::min<int64_t>(fit, (rows + kStripRows - 1) / kStripRows));
+int64_t strips_of(int64_t cols, int lanes) { return (cols + 8 * lanes - 1) / (8 * lanes); }
+
+int64_t chunks_of(int64_t rows, int64_t cols, bool gate, int sms) {
+  if (rows <= kFewRows) return 1;
+  const int lanes = lanes_of(rows, cols, gate);
+  const int64_t fit = int64_t(sms) * sum_blocks(gate) / std::max<int64_t>(1, strips_of(cols, lanes));
+  return std::max<int64_t>(1, std::min<int64_t>(fit, rows / (2 * kAbThreads / lanes)));
 }
 
 template <int DT, bool kAligned, bool kGate, bool kDb>
@@ -280,7 +299,7 @@ extern "C" size_t fp8_act_backward_workspace_bytes(int64_t rows, int64_t cols, i
   if (rows <= 0 || cols <= 0 || cols > (int64_t(1) << 30) || rows > INT32_MAX) return 0;
   const int sms = sm_count_current();
   if (sms <= 0) return 0;
-  const int64_t chunks = chunks_of(rows, cols, sms);
+  const int64_t chunks = chunks_of(rows, cols, gated != 0, sms);
   return chunks > 1 ? size_t(chunks) * size_t(cols) * 4 * (gated ? 2 : 1) : 0;
 }
 
@@ -337,8 +356,9 @@ extern "C" int fp8_act_backward(const fp8_act_backward_args* p, fp8_stream_t str
   a.duq = p->duq;
   const bool db = p->db != nullptr && some;
   if (db) {
-    a.strips = strips_of(p->cols);
-    a.chunks = chunks_of(p->rows, p->cols, sms);
+    a.lanes = lanes_of(p->rows, p->cols, ring_u);
+    a.strips = strips_of(p->cols, a.lanes);
+    a.chunks = chunks_of(p->rows, p->cols, ring_u, sms);
     a.part = p->db;  // one chunk: its sums are the result
     a.part_u = p->dbu;
     if (a.chunks > 1) {

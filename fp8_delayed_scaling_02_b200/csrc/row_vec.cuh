@@ -22,6 +22,18 @@ struct Vec8 {
 
 __device__ __forceinline__ uint4 ld16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
+// The NW words that start ph (a multiple of 2, below 16) bytes into W.
+template <int NW>
+__device__ __forceinline__ void shift_down(uint32_t (&W)[NW + 4], int ph, uint32_t* out) {
+#pragma unroll
+  for (int i = 0; i < NW + 2; ++i) W[i] = ph & 8 ? W[i + 2] : W[i];
+#pragma unroll
+  for (int i = 0; i < NW + 1; ++i) W[i] = ph & 4 ? W[i + 1] : W[i];
+  const int s = 8 * (ph & 2);
+#pragma unroll
+  for (int i = 0; i < NW; ++i) out[i] = __funnelshift_r(W[i], W[i + 1], s);
+}
+
 // Elements c .. c+7 of a row of `cols`; zeros beyond its end.
 template <int DT, bool kAligned>
 __device__ __forceinline__ Vec8<DT> load8(const uint8_t* row, int c, int cols) {
@@ -50,7 +62,7 @@ __device__ __forceinline__ Vec8<DT> load8(const uint8_t* row, int c, int cols) {
         const uint4 t = ld16(q + 16 * g);
         W[4 * g] = t.x; W[4 * g + 1] = t.y; W[4 * g + 2] = t.z; W[4 * g + 3] = t.w;
       }
-      realign<NW>(W, ph, r.w);
+      shift_down<NW>(W, ph, r.w);
       return r;
     }
 #pragma unroll
