@@ -44,7 +44,7 @@ struct ActBwdArgs {
   uint8_t* dzq;
   uint8_t* duq;
   int64_t strips;    // with sums: blockIdx.x = chunk * strips + strip
-  int lanes;         // threads across a strip, 8 columns each: 8 or 32
+  int log_lanes;     // threads across a strip, 8 columns each: 8 or 32
   int64_t chunks;
   float* part;       // [chunks][cols] sums of dz
   float* part_u;     // and of du
@@ -161,10 +161,11 @@ __global__ void __launch_bounds__(kAbThreads, kDb ? sum_blocks(kGate) : 3) act_b
   if constexpr (kDb) {
     const int64_t chunk = blockIdx.x / a.strips, strip = blockIdx.x - chunk * a.strips;
     const int cols = int(a.cols);
-    const int c = int(strip) * 8 * a.lanes + 8 * (threadIdx.x & (a.lanes - 1));
-    const int rows = kAbThreads / a.lanes;  // of one step of a block
+    const int lanes = 1 << a.log_lanes;
+    const int c = int(strip) * 8 * lanes + 8 * (threadIdx.x & (lanes - 1));
+    const int rows = kAbThreads >> a.log_lanes;  // of one step of a block
     const int64_t step = a.chunks * rows;
-    for (int64_t r = chunk * rows + threadIdx.x / a.lanes; r < a.rows; r += 2 * step) {
+    for (int64_t r = chunk * rows + (threadIdx.x >> a.log_lanes); r < a.rows; r += 2 * step) {
       const bool two = r + step < a.rows;
       load_grads<DT, kAligned>(a, r * a.cols, c, cols, g0);
       if (two) load_grads<DT, kAligned>(a, (r + step) * a.cols, c, cols, g1);
@@ -172,14 +173,16 @@ __global__ void __launch_bounds__(kAbThreads, kDb ? sum_blocks(kGate) : 3) act_b
       if (two) emit_grads<DT, kAligned, kGate, kDb>(a, (r + step) * a.cols, c, cols, g1, s, su, amax, amax_u, sum, sum_u);
     }
     // A warp's rows by shuffles (narrow strips), the warps through shared memory, in order.
-    for (int o = a.lanes; o < 32; o <<= 1) {
+    if (lanes == 8) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
-        if constexpr (kGate) sum_u[i] += __shfl_xor_sync(0xFFFFFFFFu, sum_u[i], o);
-      }
+      for (int o = 8; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
+          if constexpr (kGate) sum_u[i] += __shfl_xor_sync(0xFFFFFFFFu, sum_u[i], o);
+        }
     }
-    if (lane < a.lanes) {
+    if (lane < lanes) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         sum_s[warp * kMaxStripCols + 8 * lane + i] = sum[i];
@@ -217,7 +220,7 @@ __global__ void __launch_bounds__(kAbThreads, kDb ? sum_blocks(kGate) : 3) act_b
   }
   if constexpr (kDb) {
     const int64_t chunk = blockIdx.x / a.strips, strip = blockIdx.x - chunk * a.strips;
-    const int width = 8 * a.lanes;
+    const int width = 8 << a.log_lanes;
     const int64_t c = strip * width + threadIdx.x;
     if (threadIdx.x < width && c < a.cols) {
 #pragma unroll
@@ -356,8 +359,9 @@ extern "C" int fp8_act_backward(const fp8_act_backward_args* p, fp8_stream_t str
   a.duq = p->duq;
   const bool db = p->db != nullptr && some;
   if (db) {
-    a.lanes = lanes_of(p->rows, p->cols, ring_u);
-    a.strips = strips_of(p->cols, a.lanes);
+    const int lanes = lanes_of(p->rows, p->cols, ring_u);
+    a.log_lanes = lanes == 32 ? 5 : 3;
+    a.strips = strips_of(p->cols, lanes);
     a.chunks = chunks_of(p->rows, p->cols, ring_u, sms);
     a.part = p->db;  // one chunk: its sums are the result
     a.part_u = p->dbu;
