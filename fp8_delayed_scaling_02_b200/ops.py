@@ -159,8 +159,9 @@ class Ring:
     def __init__(self, device="cuda", scale=1.0):
         self.buf = torch.zeros(self.WORDS, dtype=torch.int32, device=device)
         f = self.buf.view(torch.float32)
-        f[17] = float(scale)
-        f[18] = 1.0
+        f[17:19].fill_(1.0)
+        if scale != 1.0:
+            f[17] = float(scale)
 
     @property
     def buf(self):
