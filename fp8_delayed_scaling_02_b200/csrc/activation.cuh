@@ -49,26 +49,6 @@ __device__ __forceinline__ float act_value(int act, float z) {
 // tile's products run, so each operation that can is a packed one.  e^-w grows
 // without bound for w << 0: its sum's reciprocal is then 0, and so is the value.
 
-__device__ __forceinline__ void mul2(float& a, float& b, float c, float d) {
-  asm("{\n\t.reg .b64 ra, rc;\n\t"
-      "mov.b64 ra, {%0, %1};\n\t"
-      "mov.b64 rc, {%2, %3};\n\t"
-      "mul.rn.f32x2 ra, ra, rc;\n\t"
-      "mov.b64 {%0, %1}, ra;\n\t}"
-      : "+f"(a), "+f"(b)
-      : "f"(c), "f"(d));
-}
-
-__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
-  asm("{\n\t.reg .b64 ra, rc;\n\t"
-      "mov.b64 ra, {%0, %1};\n\t"
-      "mov.b64 rc, {%2, %3};\n\t"
-      "add.rn.f32x2 ra, ra, rc;\n\t"
-      "mov.b64 {%0, %1}, ra;\n\t}"
-      : "+f"(a), "+f"(b)
-      : "f"(c), "f"(d));
-}
-
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -113,17 +93,6 @@ __device__ __forceinline__ void act_pair(float& a, float& b) {
 
 // value and slope of a pair: q = 1 - p is off by at most 2^-24, which the slope
 // p + z p q multiplies by |z p|.  z^2 is capped so that p q = 0 times it is 0.
-__device__ __forceinline__ void fma2v(float& a, float& b, float c, float d, float e, float f) {  // (a c + e, b d + f)
-  asm("{\n\t.reg .b64 ra, rc, re;\n\t"
-      "mov.b64 ra, {%0, %1};\n\t"
-      "mov.b64 rc, {%2, %3};\n\t"
-      "mov.b64 re, {%4, %5};\n\t"
-      "fma.rn.f32x2 ra, ra, rc, re;\n\t"
-      "mov.b64 {%0, %1}, ra;\n\t}"
-      : "+f"(a), "+f"(b)
-      : "f"(c), "f"(d), "f"(e), "f"(f));
-}
-
 template <int ACT>
 __device__ __forceinline__ void act_slope_pair(float& a, float& b, float& sa, float& sb) {
   if constexpr (ACT == FP8_ACT_NONE) {

@@ -42,6 +42,38 @@ __device__ __forceinline__ void fma2(float& a, float& b, float s, float c, float
       : "f"(s), "f"(c), "f"(d));
 }
 
+// (a*c, b*d), (a+c, b+d) and (a*c + e, b*d + f), rounded per lane.
+__device__ __forceinline__ void mul2(float& a, float& b, float c, float d) {
+  asm("{\n\t.reg .b64 ra, rc;\n\t"
+      "mov.b64 ra, {%0, %1};\n\t"
+      "mov.b64 rc, {%2, %3};\n\t"
+      "mul.rn.f32x2 ra, ra, rc;\n\t"
+      "mov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+  asm("{\n\t.reg .b64 ra, rc;\n\t"
+      "mov.b64 ra, {%0, %1};\n\t"
+      "mov.b64 rc, {%2, %3};\n\t"
+      "add.rn.f32x2 ra, ra, rc;\n\t"
+      "mov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+
+__device__ __forceinline__ void fma2v(float& a, float& b, float c, float d, float e, float f) {
+  asm("{\n\t.reg .b64 ra, rc, re;\n\t"
+      "mov.b64 ra, {%0, %1};\n\t"
+      "mov.b64 rc, {%2, %3};\n\t"
+      "mov.b64 re, {%4, %5};\n\t"
+      "fma.rn.f32x2 ra, ra, rc, re;\n\t"
+      "mov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d), "f"(e), "f"(f));
+}
+
 // fp8 codes of two already-scaled values packed low byte first.
 template <int FMT>
 __device__ __forceinline__ uint32_t cvt2(float lo, float hi) {

@@ -107,8 +107,14 @@ __device__ __forceinline__ void load_gamma8(const void* gamma, int f32, int c, i
   else unpack8<DT>(load8<DT, kAligned>(p, c, cols), g);
 }
 
+// Blocks per SM that the forward's registers allow, for the loads in flight.  Two
+// 16-bit vectors per thread, 8192 x 1536 in blocks of three, four and (126
+// registers) two: 16.6, 19.1 and 21.7 us; 8192 x 1537: 43.9, 38.9 and 56.2.
 template <int DT, bool kAligned, int V, int NT>
-__global__ void __launch_bounds__(NT) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
+constexpr int kFwdBlocks = NT > 256 ? 1 : V == 1 ? 4 : In<DT>::kBytes == 4 ? 2 : kAligned ? 3 : 4;
+
+template <int DT, bool kAligned, int V, int NT>
+__global__ void __launch_bounds__(NT, (kFwdBlocks<DT, kAligned, V, NT>)) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   constexpr int kB = In<DT>::kBytes;
   // Up to two vectors per thread: the next row's loads go out ahead of the row
   // in work, and gamma is read again for each row.  Four: gamma is kept instead.
@@ -152,42 +158,45 @@ __global__ void __launch_bounds__(NT) rmsnorm_kernel(const __grid_constant__ Nor
   if (row < a.rows) load(row);
   for (; row < a.rows; row += step) {
     const int64_t off = row * a.cols * kB;
-    Vec8<DT> h[V];
-    float ss = 0.0f;
+    float p[V][8];  // h, then v
+    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float p[8];
-      unpack8<DT>(nx[v], p);
-      h[v] = nx[v];
+      unpack8<DT>(nx[v], p[v]);
       if (a.res != nullptr) {
         float q[8];
         unpack8<DT>(nr[v], q);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] += q[i];
-        h[v] = pack8<DT>(p);
-        unpack8<DT>(h[v], p);
+        for (int i = 0; i < 8; i += 2) add2(p[v][i], p[v][i + 1], q[i], q[i + 1]);
+        unpack8<DT>(pack8<DT>(p[v]), p[v]);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(p[i], p[i], ss);
+      for (int i = 0; i < 8; i += 2) {
+        float x = p[v][i], y = p[v][i + 1];
+        fma2v(x, y, x, y, s0, s1);
+        s0 = x, s1 = y;
+      }
     }
     if (kAhead && row + step < a.rows) load(row + step);
     if (a.res != nullptr) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) store8<DT, kAligned>(a.h + off, 8 * t + v * stride, a.cols, h[v]);
+      for (int v = 0; v < V; ++v) store8<DT, kAligned>(a.h + off, 8 * t + v * stride, a.cols, pack8<DT>(p[v]));
     }
     if (kAhead) load_gamma();
-    const float rstd = rsqrtf(fmaf(gr.sum(ss), inv_cols, a.eps));
+    const float rstd = rsqrtf(fmaf(gr.sum(s0 + s1), inv_cols, a.eps));
     if (a.rstd != nullptr && t == 0) a.rstd[row] = rstd;
+    float m = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        scale2(p[v][i], p[v][i + 1], rstd);
+        mul2(p[v][i], p[v][i + 1], gm[v][i], gm[v][i + 1]);
+        m = fmaxf(m, fmaxf(fabsf(p[v][i]), fabsf(p[v][i + 1])));  // 0 beyond the row's end
+      }
+    amax = fmaxf(amax, m);
     float s = s_ring;
     if (a.row_sinv != nullptr) {
-      float m = 0.0f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float p[8];
-        unpack8<DT>(h[v], p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(__fmul_rn(__fmul_rn(p[i], rstd), gm[v][i])));
-      }
       m = gr.max(m);
       s = 1.0f;
       if (m > 0.0f && isfinite(m)) {
@@ -199,22 +208,15 @@ __global__ void __launch_bounds__(NT) rmsnorm_kernel(const __grid_constant__ Nor
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = 8 * t + v * stride;
-      float p[8];
-      unpack8<DT>(h[v], p);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = __fmul_rn(__fmul_rn(p[i], rstd), gm[v][i]);
-        amax = fmaxf(amax, fabsf(p[i]));  // 0 beyond the row's end
-      }
-      if (a.y != nullptr) store8<DT, kAligned>(a.y + off, c, a.cols, pack8<DT>(p));
+      if (a.y != nullptr) store8<DT, kAligned>(a.y + off, c, a.cols, pack8<DT>(p[v]));
       if (a.codes != nullptr) {
         uint32_t lo, hi;
         if (a.fmt == FP8_E5M2) {
-          lo = cvt4<FP8_E5M2>(p[0], p[1], p[2], p[3], s);
-          hi = cvt4<FP8_E5M2>(p[4], p[5], p[6], p[7], s);
+          lo = cvt4<FP8_E5M2>(p[v][0], p[v][1], p[v][2], p[v][3], s);
+          hi = cvt4<FP8_E5M2>(p[v][4], p[v][5], p[v][6], p[v][7], s);
         } else {
-          lo = cvt4<FP8_E4M3>(p[0], p[1], p[2], p[3], s);
-          hi = cvt4<FP8_E4M3>(p[4], p[5], p[6], p[7], s);
+          lo = cvt4<FP8_E4M3>(p[v][0], p[v][1], p[v][2], p[v][3], s);
+          hi = cvt4<FP8_E4M3>(p[v][4], p[v][5], p[v][6], p[v][7], s);
         }
         store8_codes<kAligned>(a.codes + row * a.cols, c, a.cols, lo, hi);
       }
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(const __grid_constant__
   constexpr int kB = In<DT>::kBytes;
   constexpr bool kAhead = V * kB <= 4;  // the next row's loads go out early, as far as the registers last
   __shared__ float red[2 * kRedWords];
-  extern __shared__ float sum_s[];  // [cols], where several groups' dgamma sums meet
+  extern __shared__ __align__(16) float sum_s[];  // [cols], where several groups' dgamma sums meet
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   const int warp = threadIdx.x >> 5;
@@ -270,32 +272,32 @@ __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(const __grid_constant__
   for (; row < a.rows; row += step) {
     const int64_t off = row * a.cols * kB;
     const float rstd = nrstd;
-    Vec8<DT> dy[V], h[V], dr[V];
-    float gm[V][8];
-    float dot = 0.0f;
+    Vec8<DT> dr[V];
+    float g[V][8], n[V][8];  // dy * gamma, h * rstd
+    float d0 = 0.0f, d1 = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      load_gamma8<DT, kAligned>(a.gamma, a.gamma_f32, 8 * t + v * stride, a.cols, gm[v]);
-      dy[v] = ny[v];
-      h[v] = nh[v];
+      float gm[8];
+      load_gamma8<DT, kAligned>(a.gamma, a.gamma_f32, 8 * t + v * stride, a.cols, gm);
+      unpack8<DT>(ny[v], g[v]);
+      unpack8<DT>(nh[v], n[v]);
       dr[v] = nr[v];
-      float d[8], n[8];
-      unpack8<DT>(dy[v], d);
-      unpack8<DT>(h[v], n);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = d[i] * (n[i] * rstd);
-        dg[v][i] += e;
-        dot = fmaf(e, gm[v][i], dot);
+      for (int i = 0; i < 8; i += 2) {
+        scale2(n[v][i], n[v][i + 1], rstd);
+        float x = g[v][i], y = g[v][i + 1];
+        mul2(x, y, n[v][i], n[v][i + 1]);
+        add2(dg[v][i], dg[v][i + 1], x, y);
+        fma2v(x, y, gm[i], gm[i + 1], d0, d1);
+        d0 = x, d1 = y;
+        mul2(g[v][i], g[v][i + 1], gm[i], gm[i + 1]);
       }
     }
     if (kAhead && row + step < a.rows) load(row + step);
-    const float c1 = gr.sum(dot) * inv_cols;
+    const float c1 = -(gr.sum(d0 + d1) * inv_cols);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float d[8], n[8], e[8];
-      unpack8<DT>(dy[v], d);
-      unpack8<DT>(h[v], n);
+      float e[8];
       if (a.dres != nullptr) {
         unpack8<DT>(dr[v], e);
       } else {
@@ -303,29 +305,37 @@ __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(const __grid_constant__
         for (int i = 0; i < 8; ++i) e[i] = 0.0f;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = fmaf(rstd, fmaf(-(n[i] * rstd), c1, d[i] * gm[v][i]), e[i]);
-      store8<DT, kAligned>(a.dx + off, 8 * t + v * stride, a.cols, pack8<DT>(e));
+      for (int i = 0; i < 8; i += 2) {
+        fma2(n[v][i], n[v][i + 1], c1, g[v][i], g[v][i + 1]);
+        fma2(n[v][i], n[v][i + 1], rstd, e[i], e[i + 1]);
+      }
+      store8<DT, kAligned>(a.dx + off, 8 * t + v * stride, a.cols, pack8<DT>(n[v]));
     }
     if (!kAhead && row + step < a.rows) load(row + step);
   }
   if (a.partial == nullptr) return;
   float* out = a.partial + int64_t(blockIdx.x) * a.cols;
-  if (a.groups > 1) {
+  if (a.groups > 1) {  // in order; sum_s is a whole number of vectors
     for (int q = 0; q < a.groups; ++q) {
       if (group == q) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int c = 8 * t + v * stride + i;
-            if (c >= a.cols) continue;
-            if (q > 0) dg[v][i] += sum_s[c];
-            sum_s[c] = dg[v][i];
+        for (int v = 0; v < V; ++v) {
+          const int c = 8 * t + v * stride;
+          if (c >= a.cols) continue;
+          float4* s = reinterpret_cast<float4*>(sum_s + c);
+          if (q > 0) {
+            const float4 x = s[0], y = s[1];
+            dg[v][0] += x.x, dg[v][1] += x.y, dg[v][2] += x.z, dg[v][3] += x.w;
+            dg[v][4] += y.x, dg[v][5] += y.y, dg[v][6] += y.z, dg[v][7] += y.w;
           }
+          s[0] = make_float4(dg[v][0], dg[v][1], dg[v][2], dg[v][3]);
+          s[1] = make_float4(dg[v][4], dg[v][5], dg[v][6], dg[v][7]);
+        }
       }
       __syncthreads();
     }
-    if (group != a.groups - 1) return;
+    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) out[c] = sum_s[c];
+    return;
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -404,14 +414,15 @@ int launch_fwd1(const NormArgs& a, const RowSplit& s, cudaStream_t st) {
 template <int DT, bool kAligned>
 int launch_fwd(const NormArgs& a, const RowSplit& s, cudaStream_t st) {
   if (s.v == 4) return launch_fwd1<DT, kAligned, 4, 512>(a, s, st);
-  if (s.v == 2) return launch_fwd1<DT, kAligned, 2, 512>(a, s, st);
+  if (s.v == 2)
+    return s.threads() > 256 ? launch_fwd1<DT, kAligned, 2, 512>(a, s, st) : launch_fwd1<DT, kAligned, 2, 256>(a, s, st);
   return launch_fwd1<DT, kAligned, 1, 256>(a, s, st);
 }
 
 template <int DT, bool kAligned, int V>
 int launch_bwd1(const NormBwdArgs& a, const RowSplit& s, int64_t grid, cudaStream_t st) {
   // Shared sums of several groups: at most 8192 columns, since more leave one group.
-  const size_t smem = s.groups > 1 ? size_t(a.cols) * 4 : 0;
+  const size_t smem = s.groups > 1 ? size_t((a.cols + 7) & ~7) * 4 : 0;
   const cudaError_t e = launch_pdl(rmsnorm_bwd_kernel<DT, kAligned, V, bwd_threads(In<DT>::kBytes, kAligned, V)>,
                                    dim3(unsigned(grid)), dim3(s.threads()), smem, st, 1, a);
   return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
