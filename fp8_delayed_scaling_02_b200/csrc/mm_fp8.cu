@@ -86,13 +86,16 @@ constexpr int kEpiOut8 = 1;   // EPI bit: FP8 output codes + output ring fold
 constexpr int kEpiBias8 = 2;  // EPI bit: FP8 bias codes
 constexpr int kEpiAct = 4;    // EPI bit: activation, residual or gate operand, kept pre-activation
 constexpr int kEpiZ = 8;      // EPI bit, with kEpiAct and bf16 output: z is kept
+constexpr int kEpiDirect = 16;  // EPI bit, with kEpiAct: output rows of whole 32-byte sectors, written by their lanes
 template <int BN, int PAIR, int EPI>
 struct ActCfg : Cfg<BN, PAIR> {
   using B = Cfg<BN, PAIR>;
   static constexpr int kWarps = BN / 16;
   static constexpr int kThreads = 32 * (2 + kWarps);
-  static constexpr int kBufA = 4096, kBufB = EPI & kEpiOut8 ? 2048 : EPI & kEpiZ ? 4096 : 0;
-  static constexpr int kStages = (232448 - 512 - 1024 - kWarps * (kBufA + kBufB)) / B::kStageBytes;
+  static constexpr int kBufA = 4096;
+  static constexpr int kBufB = EPI & kEpiDirect ? 0 : EPI & kEpiOut8 ? 2048 : EPI & kEpiZ ? 4096 : 0;
+  static constexpr int kFit = (232448 - 512 - 1024 - kWarps * (kBufA + kBufB)) / B::kStageBytes;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kStagingOffset = kStages * B::kStageBytes;
   static constexpr int kBarOffset = kStagingOffset + kWarps * (kBufA + kBufB);
   static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
@@ -287,6 +290,12 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
 }
 __device__ __forceinline__ void ld_shared16(uint32_t addr, uint32_t* v) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+}
+// 32 bytes, a whole sector, per lane.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read_le1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
@@ -629,13 +638,14 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
                                               const uint32_t tmem_base, const uint32_t bar0, volatile int* abort) {
   using C = ActCfg<BN, PAIR, EPI>;
   constexpr bool kOut8 = (EPI & kEpiOut8) != 0;
+  constexpr bool kDirect = (EPI & kEpiDirect) != 0;
   const int part = ew >> 2;
   const uint32_t tfull0 = bar0 + 8u * (2 * C::kStages), tempty0 = tfull0 + 16u;
   const uint32_t stall_bar = bar0 + 8u * C::kStallBar;
   const uint32_t aux_bar = bar0 + 256u + 8u * ew;
   const uint32_t bufa = staging + uint32_t(ew) * C::kBufA;
   const uint32_t bufb = staging + uint32_t(C::kWarps) * C::kBufA + uint32_t(ew) * C::kBufB;
-  const bool has_z = kOut8 ? p.z != nullptr : (EPI & kEpiZ) != 0;
+  const bool has_z = kOut8 || kDirect ? p.z != nullptr : (EPI & kEpiZ) != 0;
   // z lies over the aux units when codes leave, beside them when y does.
   const uint32_t zbuf = kOut8 ? bufa : bufb;
   // This lane's row of the buffers (unit128's and unit64's layout).
@@ -686,6 +696,7 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
       bias_l.x = __ldg(p.bias + t.n0 + 2 * lane);
       if (2 * lane + 1 < cols) bias_l.y = __ldg(p.bias + t.n0 + 2 * lane + 1);
     }
+    const int64_t at = int64_t(m) * p.N + t.n0;  // this lane's row
     if (has_aux && t.any) {
       if (prefetch) {
         bool ok = mbar_wait(aux_bar, aux_par, abort, p.err, kWaitEpilogueAux, p.wait_ns);
@@ -708,6 +719,7 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
     tc_fence_after();
     __syncwarp();
     const uint32_t tbase = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + part * 64);
+    uint32_t code[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // the last two sixteens
     // Not unrolled: the body stays in the instruction cache's first level.
 #pragma unroll 1
     for (int h = 0; 16 * h < cols; ++h) {
@@ -737,7 +749,15 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
         const __nv_bfloat162 v = __floats2bfloat162_rn(y[j], y[j + 1]);
         return *reinterpret_cast<const uint32_t*>(&v);
       };
-      if (has_z) {
+      auto pack16 = [&](uint32_t (&v)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = pack(2 * j);
+      };
+      if (kDirect && has_z) {
+        uint32_t v[8];
+        pack16(v);
+        if (row_ok) st_global32(p.z + at + 16 * h, v);
+      } else if (has_z) {
         st_shared16(rowz + (uint32_t(32 * h) ^ swz), pack(0), pack(2), pack(4), pack(6));
         st_shared16(rowz + (uint32_t(32 * h + 16) ^ swz), pack(8), pack(10), pack(12), pack(14));
       }
@@ -764,12 +784,21 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
 #pragma unroll
         for (int j = 0; j < 16; j += 2) m16 = fmaxf(m16, fmaxf(fabsf(y[j]), fabsf(y[j + 1])));
         if (row_ok) amax = fmaxf(amax, m16);
-        uint32_t code[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) code[j] = code[j + 4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          code[j] = p.out_fmt == FP8_E5M2 ? cvt4<FP8_E5M2>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out)
+          code[j + 4] = p.out_fmt == FP8_E5M2 ? cvt4<FP8_E5M2>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out)
                                           : cvt4<FP8_E4M3>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out);
-        st_shared16(rowb + (uint32_t(16 * h) ^ swz8), code[0], code[1], code[2], code[3]);
+        if constexpr (kDirect) {
+          if ((h & 1) && row_ok) st_global32(p.out8 + at + 16 * (h - 1), code);
+        } else {
+          st_shared16(rowb + (uint32_t(16 * h) ^ swz8), code[4], code[5], code[6], code[7]);
+        }
+      } else if constexpr (kDirect) {
+        uint32_t v[8];
+        pack16(v);
+        if (row_ok) st_global32(p.out + at + 16 * h, v);
       } else {
         st_shared16(rowa + (uint32_t(32 * h) ^ swz), pack(0), pack(2), pack(4), pack(6));
         st_shared16(rowa + (uint32_t(32 * h + 16) ^ swz), pack(8), pack(10), pack(12), pack(14));
@@ -780,6 +809,10 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
     __syncwarp();
     if (lane == 0) mbar_arrive_cluster(PAIR == 1 ? tempty0 + 8u * acc : mapa_shared(tempty0 + 8u * acc, 0));
     if (!t.any) continue;
+    if constexpr (kDirect) {
+      if (prefetch) ask();  // every lane has read the buffer
+      continue;
+    }
     if (has_z && !p.z_tma) store_rows_bf16(p, p.z, zbuf, t, lane);
     if (!p.tma_store) {
       if constexpr (kOut8) store_rows_codes(p, bufb, t, lane);
@@ -1681,6 +1714,7 @@ template <int BN, int PAIR, int EPI>
 int launch_act_epi(const MmProblem& q, const MmChoice& c, cudaStream_t st) {
   CUtensorMap ta, tb, tc, tx, tz;
   MmParams p = q.p;
+  if (EPI & kEpiDirect) p.tma_store = p.z_tma = 0;  // no map of these
   const int rc = prepare_mm<BN, PAIR>(q.A, q.B, q.M, q.N, q.K, 1, nullptr, p, c, nullptr, ta, tb, tc);
   if (rc != FP8_OK) return rc;
   p.inv_span = 1.0f / float(8 * p.n_tiles);
@@ -1704,9 +1738,25 @@ int launch_act_epi(const MmProblem& q, const MmChoice& c, cudaStream_t st) {
   return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
+// z or codes in rows of whole 32-byte sectors, at bases that are too, are
+// written by the lanes that hold them: no staging, and its shared memory goes to
+// a stage (8192 x 4096 x 1536 gated, z kept, codes out: 59.4 us, staged 62.5;
+// the same with aux read by its lanes: 64.7).  A bf16 output alone is formed in
+// the aux buffer and leaves by TMA as fast or faster (8192 x 4096 x 128: 16.9
+// us, direct 19.6).
+bool act_direct(const MmProblem& q) {
+  const MmParams& p = q.p;
+  return (p.out8 != nullptr || p.z != nullptr) && q.N % (p.out8 ? 32 : 16) == 0 && on(p.z, 32) && on(p.out8, 32) &&
+         on(p.out, 32);
+}
+
 template <int BN, int PAIR>
 int launch_act(const MmProblem& q, const MmChoice& c, cudaStream_t st) {
-  if (q.epi & kEpiOut8) return launch_act_epi<BN, PAIR, kEpiAct | kEpiOut8>(q, c, st);
+  const bool out8 = (q.epi & kEpiOut8) != 0;
+  if (act_direct(q))
+    return out8 ? launch_act_epi<BN, PAIR, kEpiAct | kEpiDirect | kEpiOut8>(q, c, st)
+                : launch_act_epi<BN, PAIR, kEpiAct | kEpiDirect>(q, c, st);
+  if (out8) return launch_act_epi<BN, PAIR, kEpiAct | kEpiOut8>(q, c, st);
   return q.p.z != nullptr ? launch_act_epi<BN, PAIR, kEpiAct | kEpiZ>(q, c, st)
                           : launch_act_epi<BN, PAIR, kEpiAct>(q, c, st);
 }
