@@ -527,17 +527,21 @@ __device__ __forceinline__ void decode_tile(const MmParams& p, int t, int& b, in
 //
 // y = act(z) [+ or * aux] for z = acc * sinv + bias.  Each epilogue warp has the
 // 32 x 64 piece of every tile at its TMEM lane quadrant and its quarter of the
-// columns (half, or all, of narrower tiles).  The aux piece is in the warp's
-// buffer before the tile's products are: a TMA load for the next tile goes out
-// as soon as this tile's stores have read the buffer.  Sixteen columns at a
-// time: TMEM -> z -> act -> y, written over the aux units just read (codes
-// beside them); then one group of TMA stores.
-// Rows of a box are 128 bytes: an SM's TMA unit takes a row of a box about
-// every four cycles however short it is, and 64-byte rows (32 columns a box)
-// made the epilogue of an 8192 x 4096 output 46 us long by itself (K = 128,
-// gated, z kept), more than the products of K = 1536.
-// Tensors whose rows are not 16-byte multiples go through the same buffers by
-// guarded accesses of one row at a time.
+// columns (half, or all, of narrower tiles), a lane a row: one warp per piece,
+// since a piece is a chain of TMEM, shared memory and MUFU latencies (eight
+// warps with two pieces each took 54 us for the epilogue of 8192 x 4096 alone,
+// sixteen 46).  The aux piece is in the warp's buffer before the tile's products
+// are: a TMA load for the next tile, into L2 while this tile is in work, goes
+// out as soon as the buffer is free.  Sixteen columns at a time: TMEM -> z ->
+// act -> y; then
+//   * direct: z and codes go from the registers to global memory, 32 bytes of a
+//     row per lane;
+//   * staged: z and y lie over the aux units just read, or beside them, and
+//     leave by TMA; rows that are no 16-byte multiples by guarded accesses.
+// What bounds it, 8192 x 4096 x 1536 gated, z kept, codes out, 59.7 us: the way
+// from L2 to the SMs.  The tiles' operands are 403 MB, aux, z and the codes 168
+// MB more, and each of aux and z adds what it moves (45.5 us without either,
+// 52.1 with z, 53.1 with aux), whichever unit moves it; silu adds 1 us.
 
 struct ActPiece {
   int i, m0, n0;  // tile ordinal of this CTA; first row and column of this warp's piece
