@@ -109,6 +109,10 @@ __device__ __forceinline__ void emit_grads(const ActBwdArgs& a, int64_t e, int c
       mul2(d[i], d[i + 1], u[i], u[i + 1]);
     }
   }
+  if (a.act == FP8_ACT_RELU) {  // nothing passes where the slope is 0, not even 0 times an infinity
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = sl[i] == 0.0f ? 0.0f : d[i];
+  }
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     mul2(d[i], d[i + 1], sl[i], sl[i + 1]);

@@ -1,14 +1,14 @@
 // Activations of the product's epilogue and their slopes, in float32.
 //
-//   relu  max(z, 0)                       slope z > 0
+//   relu  max(z, 0)                       slope 0 for z <= 0, else 1
 //   silu  z p,  p = 1 / (1 + e^-z)        slope p + z p q,  q = 1 - p
 //   gelu  z p,  p = 1 / (1 + e^-w),       slope p + z p q w'
 //         w = 2 sqrt(2/pi) (z + 0.044715 z^3): the tanh form, since
 //         (1 + tanh(w/2)) / 2 is the logistic function of w
 //
-// logistic: p and q both come from t = e^-|w| in (0, 1]: r = 1/(1+t) is one of them and
-// t r the other, so neither cancels nor overflows, however large |w|.  The
-// fast exponential and division are within (2 + 1.2 |w|) and 2 float32 ulp
+// act_value, for single values: p and q both come from t = e^-|w| in (0, 1]: r =
+// 1/(1+t) is one of them and t r the other, so neither cancels nor overflows.
+// The fast exponential and division are within (2 + 1.2 |w|) and 2 float32 ulp
 // (CUDA's stated bounds): far inside what the 8- and 16-bit outputs keep.
 #pragma once
 
@@ -21,24 +21,20 @@ namespace fp8ds {
 constexpr float kGeluC2 = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGeluA = 0.044715f;
 
-__device__ __forceinline__ void logistic(float w, float& p, float& q) {
+__device__ __forceinline__ float logistic(float w) {
   const float t = __expf(-fabsf(w));
   const float r = __fdividef(1.0f, 1.0f + t);
-  const float tr = t * r;
-  p = w >= 0.0f ? r : tr;
-  q = w >= 0.0f ? tr : r;
-  if (w != w) p = w;
+  return w < 0.0f ? t * r : r;  // NaN: r is NaN
 }
 
 // z^2, kept finite so that 0 * z^2 stays 0 where p q has vanished.
 __device__ __forceinline__ float square_capped(float z) { return fminf(z * z, 1.0e30f); }
 
 __device__ __forceinline__ float act_value(int act, float z) {
-  float p, q;
   switch (act) {
     case FP8_ACT_RELU: return z < 0.0f ? 0.0f : z;  // NaN stays NaN
-    case FP8_ACT_SILU: logistic(z, p, q); return z * p;
-    case FP8_ACT_GELU: logistic(z * fmaf(kGeluC2 * kGeluA, square_capped(z), kGeluC2), p, q); return z * p;
+    case FP8_ACT_SILU: return z * logistic(z);
+    case FP8_ACT_GELU: return z * logistic(z * fmaf(kGeluC2 * kGeluA, square_capped(z), kGeluC2));
     default: return z;
   }
 }
@@ -98,8 +94,8 @@ __device__ __forceinline__ void act_slope_pair(float& a, float& b, float& sa, fl
   if constexpr (ACT == FP8_ACT_NONE) {
     sa = sb = 1.0f;
   } else if constexpr (ACT == FP8_ACT_RELU) {
-    sa = a > 0.0f ? 1.0f : 0.0f;
-    sb = b > 0.0f ? 1.0f : 0.0f;
+    sa = a <= 0.0f ? 0.0f : 1.0f;
+    sb = b <= 0.0f ? 0.0f : 1.0f;
     a = max_nan(a, 0.0f);
     b = max_nan(b, 0.0f);
   } else {

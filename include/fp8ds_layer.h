@@ -107,7 +107,8 @@ int fp8_rmsnorm_backward(const fp8_rmsnorm_backward_args* args, fp8_stream_t str
 size_t fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
 
 /* Activations of fp8_mm_act and fp8_act_backward: value and slope at z.
- *   RELU  max(z, 0), slope 1 for z > 0, else 0
+ *   RELU  max(z, 0), slope 0 for z <= 0, else 1; where it is 0, dz is 0
+ *         whatever dy and u are
  *   GELU  the tanh form: z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
  *   SILU  z / (1 + e^-z) */
 typedef enum { FP8_ACT_NONE = 0, FP8_ACT_RELU = 1, FP8_ACT_GELU = 2, FP8_ACT_SILU = 3 } fp8_act;
@@ -134,7 +135,9 @@ typedef enum { FP8_AUX_ADD = 0, FP8_AUX_MUL = 1 } fp8_aux_op;
  * bias    float32 [N] or NULL.  aux: bf16 [M, N] or NULL.  All contiguous.
  *         out may be aux itself (a residual stream updated in place).
  * M, N >= 0, K >= 0 with K % 16 == 0; K == 0 gives z = bias; an empty output
- * still folds amax 0.
+ * still folds amax 0.  A few rows of A (16, or 32 with few columns) take a
+ * kernel that reads B once, straight into registers; its sums run in another
+ * order than the tile kernel's, within the same bound.
  * Errors as fp8_mm_ex; FP8_ERR_INVALID_ARG also for an unknown act or aux_op,
  *         other layout bits, an output that overlaps another argument;
  *         FP8_ERR_UNSUPPORTED for an address not aligned to its element.

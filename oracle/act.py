@@ -30,7 +30,7 @@ def slope(z, kind):
     """d act / dz."""
     z = np.asarray(z, dtype=np.float64)
     if kind == RELU:
-        return (z > 0).astype(np.float64)
+        return np.where(z <= 0, 0.0, 1.0)
     with np.errstate(over="ignore"):
         if kind == GELU:
             # (1 + tanh(w/2)) / 2 = p and (1 - tanh^2) / 4 = p q, again without cancellation
@@ -79,8 +79,8 @@ def _relative(z, kind):
 def backward(dy, z, kind, u=None):
     """(dz, du) of y = act(z) [* u]; du is None without u."""
     dy = np.asarray(dy, dtype=np.float64)
-    d = dy * slope(z, kind)
-    if u is None:
-        return d, None
-    u = np.asarray(u, dtype=np.float64)
-    return d * u, dy * act(z, kind)
+    d = dy if u is None else dy * np.asarray(u, dtype=np.float64)
+    s = slope(z, kind)
+    if kind == RELU:
+        d = np.where(s == 0, 0.0, d)  # nothing passes where the slope is 0
+    return d * s, None if u is None else dy * act(z, kind)

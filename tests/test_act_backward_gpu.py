@@ -117,6 +117,39 @@ def test_act_backward_of_huge_and_special_pre_activations():
         assert float(ring.state()[0][0]) == 1.0  # a NaN does not enter the amax
 
 
+def test_relu_lets_nothing_through_where_it_is_zero():
+    """Infinite and NaN gradients (and gates) where z <= 0 reach neither dz, nor its amax, nor the sums."""
+    bad = float("inf"), float("-inf"), float("nan")
+    z = torch.tensor([[-1.0, -0.0, 0.0, 2.0]] * 3, dtype=torch.bfloat16)
+    for db in (False, True):
+        for gate in (False, True):
+            dy = torch.tensor([[b, b, b, 1.0] for b in bad], dtype=torch.bfloat16)
+            u = torch.tensor([[b, b, b, 3.0] for b in bad[::-1]], dtype=torch.bfloat16) if gate else None
+            ring, ring_u = ops.Ring(), ops.Ring() if gate else None
+            r = ops.act_backward(dy.cuda(), z.cuda(), ops.ACT_RELU, ops.E4M3, ring, None if u is None else u.cuda(),
+                                 ring_u, need_db=db)
+            got = r.dz.view(torch.float8_e4m3fn).float().cpu()
+            assert got.tolist() == [[0, 0, 0, 3.0 if gate else 1.0]] * 3
+            assert float(ring.state()[0][0]) == (3.0 if gate else 1.0)
+            assert not db or r.db.tolist() == [0, 0, 0, 9.0 if gate else 3.0]
+
+
+@pytest.mark.parametrize("db", [False, True])
+def test_act_backward_offsets_beyond_31_bits(db):
+    rows, cols = 70000, 32768  # 2.29e9 elements
+    tail = _inputs(3, cols, "bf16", 5, False)
+    dy, z = (torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dy[-3:].copy_(tail[0])
+    z[-3:].copy_(tail[1])
+    ring = ops.Ring(scale=30.0)
+    r = ops.act_backward(dy, z, ops.ACT_SILU, ops.E5M2, ring, need_db=db)
+    want = ops.act_backward(dy[-3:].clone(), z[-3:].clone(), ops.ACT_SILU, ops.E5M2, ops.Ring(scale=30.0), need_db=db)
+    torch.cuda.synchronize()
+    assert torch.equal(r.dz[-3:], want.dz) and not r.dz[:3].any() and not r.dz[-6:-3].any()
+    if db:  # the zeros add nothing
+        assert_within(f64(r.db), f64(want.db), 4 * U * np.abs(f64(tail[0])).sum(0) * 1.2, "db")
+
+
 def test_act_backward_empty_batch():
     for u, ring_u in ((None, None), (torch.empty(0, 40, dtype=torch.bfloat16, device="cuda"), ops.Ring(scale=3.0))):
         ring = ops.Ring(scale=2.0)

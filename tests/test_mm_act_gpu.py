@@ -129,6 +129,41 @@ def test_mm_act_training_sizes(M, N, K, act, aux_op, out_fmt):
     _check(p, act, aux_op, out_fmt, pick=band_rows(M, 1))
 
 
+@pytest.mark.parametrize("out_fmt,N", [(None, 32768), (ops.E4M3, 32768), (ops.E4M3, 32769)])
+def test_mm_act_offsets_beyond_31_bits(out_fmt, N):
+    """2.29e9 outputs; direct, staged and guarded stores."""
+    M, K = 70000, 16
+    p = _problem(128, N, K, 11, aux=False)
+    a = p["a"].repeat((M + 127) // 128, 1)[:M].contiguous().cuda()
+    b, sa, sb, bias = (p[k].cuda() for k in ("b", "sinv_a", "sinv_b", "bias"))
+    ring, ring2 = (ops.Ring(scale=3.0) if out_fmt is not None else None for _ in range(2))
+    out, _ = ops.mm_act(a, b, sa, sb, ops.ACT_GELU, bias=bias, out_fmt=out_fmt, out_ring=ring)
+    want, _ = ops.mm_act(a[:128].contiguous(), b, sa, sb, ops.ACT_GELU, bias=bias, out_fmt=out_fmt, out_ring=ring2)
+    torch.cuda.synchronize()
+    for m in (0, 128, 65536, M // 128 * 128 - 128):  # rows repeat every 128
+        assert torch.equal(out[m:m + 128], want), m
+    last = M // 128 * 128
+    assert torch.equal(out[last:], want[:M - last])
+
+
+@pytest.mark.parametrize("M,N,aux", [(128, 256, False), (128, 256, True), (600, 1024, True), (600, 1000, True)])
+def test_mm_act_wait_runs_out_then_the_next_call_is_right(M, N, aux):
+    """The timeout path (see the timeout tests of the product): the stopped kernel lets its
+    operand loads land, frees what it holds and returns; the next call is whole."""
+    p = _problem(M, N, 4096, 12, aux=aux)
+    torch.cuda.synchronize()
+    assert ops.device_error(clear=True)[0] == ops.FP8_OK
+    ops.debug_wait(20_000, ops.SITE_EPILOGUE_TMEM_FULL)
+    try:
+        _run(p, ops.ACT_SILU, ops.AUX_MUL, ops.E4M3, ops.Ring())
+        torch.cuda.synchronize()
+    finally:
+        ops.debug_wait()
+    rc, where = ops.device_error(clear=True)
+    assert rc == ops.FP8_ERR_DEVICE_TIMEOUT and where == ops.SITE_EPILOGUE_TMEM_FULL, (rc, where)
+    _check(p, ops.ACT_SILU, ops.AUX_MUL, ops.E4M3)
+
+
 def test_mm_act_without_anything_is_mm():
     """No activation, no operand: bit for bit the framework's product, where both take the tile kernel."""
     for M, N, K in ((300, 512, 256), (1000, 1537, 512)):
