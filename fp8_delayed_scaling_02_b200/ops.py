@@ -9,6 +9,7 @@ device memory and the current stream.
 import ctypes
 import functools
 import os
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -200,9 +201,13 @@ class Ring:
         return self.buf[20:24]
 
     @functools.cached_property
-    def _c(self):
+    def _addresses(self):
         base = self.buf.data_ptr()
-        return CRing(base, base + 16 * 4, base + 17 * 4, base + 18 * 4, base + 20 * 4)
+        return base, base + 16 * 4, base + 17 * 4, base + 18 * 4, base + 20 * 4
+
+    @functools.cached_property
+    def _c(self):
+        return CRing(*self._addresses)
 
     def c(self):
         return self._c
@@ -624,6 +629,35 @@ class Linear:
 
 
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+# A call on small tensors takes as long as its launch and its outputs' allocation
+# take the host: this is torch.empty on the current device at half its cost.
+_empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+if _empty_strided is None:
+    def _empty_strided(size, stride, dtype):
+        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+
+
+def _empty(n, dtype):
+    return _empty_strided((n,), (1,), dtype)
+
+
+def _empty2(rows, cols, dtype):
+    return _empty_strided((rows, cols), (cols, 1), dtype)
+
+
+def _adr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+_NO_RING = (0, 0, 0, 0, 0)
+
+
+def _packer(cls):
+    """Packs a ctypes structure's fields, a ring's five pointers one by one, into bytes: what
+    the structure itself would hold, in a quarter of the time."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_size_t: "N",
+             CRing: "PPPPP"}
+    return struct.Struct("@" + "".join(codes[f] for _, f in cls._fields_)).pack
 
 
 def _on_stream(fn):
@@ -632,9 +666,10 @@ def _on_stream(fn):
 
     @functools.wraps(fn)
     def call(x, *args, stream=None, **kw):
-        if not x.is_cuda:
+        dev = x.get_device()
+        if dev < 0:
             raise ValueError("the tensors must be CUDA tensors")
-        if stream is None and x.get_device() == _current_device():
+        if stream is None and dev == _current_device():
             return fn(x, *args, **kw)
         if stream is not None and stream.device != x.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
@@ -644,18 +679,12 @@ def _on_stream(fn):
     return call
 
 
-def _same(t, like, name, shape=None, dtype=None):
-    """Checks an optional tensor: on ``like``'s device, contiguous, of this shape and type."""
-    if t is None:
+def _same(t, dev, name, shape, dtype):
+    """Checks an optional tensor: on this device, contiguous, of this shape and type."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
         return
-    if shape is None:
-        shape = like.shape
-    if dtype is None:
-        dtype = like.dtype
-    if t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device() and t.is_contiguous():
-        return
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
@@ -663,25 +692,32 @@ def _same(t, like, name, shape=None, dtype=None):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _scalar(t, like, name):
-    if t is not None and (t.get_device() != like.get_device() or t.dtype is not torch.float32 or t.numel() != 1):
-        raise ValueError(f"{name} must be a one-element float32 tensor on {like.device}")
+def _scalar(t, dev, name):
+    if t is not None and (t.get_device() != dev or t.dtype is not torch.float32 or t.numel() != 1):
+        raise ValueError(f"{name} must be a one-element float32 tensor on cuda:{dev}")
 
 
-def _ring_on(ring, like, name):
-    if ring is not None and ring.buf.get_device() != like.get_device():
-        raise ValueError(f"{name} is on {ring.buf.device}, expected {like.device}")
+def _ring_on(ring, dev, name):
+    if ring.buf.get_device() != dev:
+        raise ValueError(f"{name} is on {ring.buf.device}, expected cuda:{dev}")
 
 
-def _gamma_checked(gamma, x):
-    if x.dtype not in IN_DTYPE:
+def _matrix(x, name):
+    """(rows, cols, type code) of a contiguous 2-D tensor of one of the three input types."""
+    code = IN_DTYPE.get(x.dtype)
+    if code is None:
         raise ValueError(f"{x.dtype} is not one of bfloat16, float16, float32")
     if x.dim() != 2 or not x.is_contiguous():
-        raise ValueError("x must be a contiguous 2-D tensor")
-    if gamma.dtype != x.dtype and gamma.dtype != torch.float32:
-        raise ValueError(f"gamma is {gamma.dtype}, expected {x.dtype} or float32")
-    _same(gamma, x, "gamma", (x.shape[1],), gamma.dtype)
-    return 1 if gamma.dtype == torch.float32 else 0
+        raise ValueError(f"{name} must be a contiguous 2-D tensor")
+    rows, cols = x.shape
+    return rows, cols, code
+
+
+def _gamma_f32(gamma, dev, cols, dtype):
+    if gamma.dtype is not dtype and gamma.dtype is not torch.float32:
+        raise ValueError(f"gamma is {gamma.dtype}, expected {dtype} or float32")
+    _same(gamma, dev, "gamma", (cols,), gamma.dtype)
+    return 1 if gamma.dtype is torch.float32 else 0
 
 
 class CNormArgs(ctypes.Structure):
@@ -704,7 +740,7 @@ class NormOut(NamedTuple):
     y: Optional[torch.Tensor]      # the norm's output in x's type
 
 
-_NO_RING = CRing()
+_pack_norm = _packer(CNormArgs)
 
 
 @_on_stream
@@ -722,42 +758,45 @@ def rmsnorm(x, gamma, residual=None, eps=1e-6, fmt=None, ring=None, need_rstd=Fa
     Returns a NormOut; ``sinv`` goes with the codes to ``mm`` or ``mm_act``
     (a scale per row to ``mm_act`` only).
     """
-    f32 = _gamma_checked(gamma, x)
-    rows, cols = x.shape
-    _same(residual, x, "residual")
+    rows, cols, code = _matrix(x, "x")
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    f32 = _gamma_f32(gamma, dev, cols, dtype)
     if residual is not None:
+        _same(residual, dev, "residual", shape, dtype)
         if h is None:
-            h = torch.empty_like(x)
+            h = _empty2(rows, cols, dtype)
         else:
-            _same(h, x, "h")
+            _same(h, dev, "h", shape, dtype)
     elif h is not None:
         raise ValueError("h needs a residual: without one it is x")
     if y is not None:
-        _same(y, x, "y")
+        _same(y, dev, "y", shape, dtype)
     elif need_y or fmt is None:
-        y = torch.empty_like(x)
-    rstd = x.new_empty(rows, dtype=torch.float32) if need_rstd else None
+        y = _empty2(rows, cols, dtype)
+    rstd = _empty(rows, torch.float32) if need_rstd else None
     sinv = row_sinv = None
     if fmt is None:
         if ring is not None or codes is not None or amax is not None:
             raise ValueError("codes, ring and amax need fmt")
     else:
         if codes is None:
-            codes = torch.empty_like(x, dtype=torch.uint8)
+            codes = _empty2(rows, cols, torch.uint8)
         else:
-            _same(codes, x, "codes", None, torch.uint8)
-        _scalar(amax, x, "amax")
+            _same(codes, dev, "codes", shape, torch.uint8)
         if ring is not None:
-            _ring_on(ring, x, "ring")
+            _ring_on(ring, dev, "ring")
+            _scalar(amax, dev, "amax")
             sinv = ring.scale_inv
         elif amax is not None:
             raise ValueError("amax needs a ring")
         else:
-            sinv = row_sinv = x.new_empty(rows, dtype=torch.float32)
-    a = CNormArgs(x.data_ptr(), _ptr(residual), IN_DTYPE[x.dtype], rows, cols, gamma.data_ptr(), f32, eps, _ptr(h),
-                  _ptr(y), _ptr(rstd), _ptr(codes), fmt or 0, ring.c() if ring is not None else _NO_RING, _ptr(amax),
-                  _ptr(row_sinv))
-    _check((_LIB or lib()).fp8_rmsnorm(ctypes.byref(a), _raw_stream(x.get_device())), "fp8_rmsnorm")
+            sinv = row_sinv = _empty(rows, torch.float32)
+    args = _pack_norm(x.data_ptr(), _adr(residual), code, rows, cols, gamma.data_ptr(), f32, eps, _adr(h), _adr(y),
+                      _adr(rstd), _adr(codes), fmt or 0, *(_NO_RING if ring is None else ring._addresses), _adr(amax),
+                      _adr(row_sinv))
+    rc = (_LIB or lib()).fp8_rmsnorm(args, _raw_stream(dev))
+    if rc:
+        _check(rc, "fp8_rmsnorm")
     return NormOut(codes, sinv, x if h is None else h, rstd, y)
 
 
@@ -770,6 +809,9 @@ class CNormBwdArgs(ctypes.Structure):
                 ("dgamma", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+_pack_norm_bwd = _packer(CNormBwdArgs)
+
+
 @_on_stream
 def rmsnorm_backward(dy, h, rstd, gamma, dres=None, dx=None, need_dgamma=True):
     """fp8_rmsnorm_backward: (dx, dgamma) of ``rmsnorm`` from its h and rstd.
@@ -778,26 +820,29 @@ def rmsnorm_backward(dy, h, rstd, gamma, dres=None, dx=None, need_dgamma=True):
     gradient that reaches h past the norm.  dy, h, dres and dx have one type;
     dx may be dy or dres (in place).  dgamma is float32 [cols], or None.
     """
-    f32 = _gamma_checked(gamma, h)
-    rows, cols = h.shape
-    _same(dy, h, "dy")
-    _same(dres, h, "dres")
-    _same(rstd, h, "rstd", (rows,), torch.float32)
+    rows, cols, code = _matrix(h, "h")
+    shape, dtype, dev = h.shape, h.dtype, h.get_device()
+    f32 = _gamma_f32(gamma, dev, cols, dtype)
+    _same(dy, dev, "dy", shape, dtype)
+    _same(dres, dev, "dres", shape, dtype)
+    _same(rstd, dev, "rstd", (rows,), torch.float32)
     if dx is None:
-        dx = torch.empty_like(h)
+        dx = _empty2(rows, cols, dtype)
     else:
-        _same(dx, h, "dx")
+        _same(dx, dev, "dx", shape, dtype)
     L = _LIB or lib()
     dgamma = ws = None
     wsb = 0
     if need_dgamma:
-        dgamma = h.new_empty(cols, dtype=torch.float32)
+        dgamma = _empty(cols, torch.float32)
         wsb = L.fp8_rmsnorm_backward_workspace_bytes(rows, cols)
         if wsb:
-            ws = h.new_empty(wsb, dtype=torch.uint8)
-    a = CNormBwdArgs(dy.data_ptr(), h.data_ptr(), _ptr(dres), IN_DTYPE[h.dtype], rows, cols, rstd.data_ptr(),
-                     gamma.data_ptr(), f32, dx.data_ptr(), _ptr(dgamma), _ptr(ws), wsb)
-    _check(L.fp8_rmsnorm_backward(ctypes.byref(a), _raw_stream(h.get_device())), "fp8_rmsnorm_backward")
+            ws = _empty(wsb, torch.uint8)
+    args = _pack_norm_bwd(dy.data_ptr(), h.data_ptr(), _adr(dres), code, rows, cols, rstd.data_ptr(), gamma.data_ptr(),
+                          f32, dx.data_ptr(), _adr(dgamma), _adr(ws), wsb)
+    rc = L.fp8_rmsnorm_backward(args, _raw_stream(dev))
+    if rc:
+        _check(rc, "fp8_rmsnorm_backward")
     return dx, dgamma
 
 
@@ -810,6 +855,9 @@ class CMmActArgs(ctypes.Structure):
                 ("act", ctypes.c_int), ("aux", ctypes.c_void_p), ("aux_op", ctypes.c_int), ("z", ctypes.c_void_p),
                 ("out_kind", ctypes.c_int), ("out", ctypes.c_void_p), ("out_ring", CRing),
                 ("out_amax", ctypes.c_void_p)]
+
+
+_pack_mm_act = _packer(CMmActArgs)
 
 
 @_on_stream
@@ -826,21 +874,23 @@ def mm_act(a, b, sinv_a, sinv_b, act=ACT_NONE, bias=None, aux=None, aux_op=AUX_A
     in bf16 for ``act_backward``.  out may be aux (in place).
     Returns (out, z); z is None when not asked for.
     """
-    if a.dtype != torch.uint8 or b.dtype != torch.uint8 or a.dim() != 2 or b.dim() != 2:
+    if a.dtype is not torch.uint8 or b.dtype is not torch.uint8 or a.dim() != 2 or b.dim() != 2:
         raise ValueError("a and b are 2-D uint8 FP8 codes")
     (M, K), (N, Kb) = a.shape, b.shape
     if Kb != K:
         raise ValueError("K mismatch")
-    if not a.is_contiguous() or not b.is_contiguous() or b.device != a.device:
+    dev = a.get_device()
+    if not a.is_contiguous() or not b.is_contiguous() or b.get_device() != dev:
         raise ValueError("a and b must be contiguous, on one device")
     na = sinv_a.numel()
     if na != 1 and na != M:
         raise ValueError(f"sinv_a has {na} elements, expected 1 or {M}")
-    _same(sinv_a, a, "sinv_a", sinv_a.shape, torch.float32)
-    _scalar(sinv_b, a, "sinv_b")
-    _same(bias, a, "bias", (N,), torch.float32)
-    _same(aux, a, "aux", (M, N), torch.bfloat16)
-    _scalar(out_amax, a, "out_amax")
+    _same(sinv_a, dev, "sinv_a", sinv_a.shape, torch.float32)
+    _scalar(sinv_b, dev, "sinv_b")
+    if bias is not None:
+        _same(bias, dev, "bias", (N,), torch.float32)
+    if aux is not None:
+        _same(aux, dev, "aux", (M, N), torch.bfloat16)
     if out_fmt is None:
         if out_ring is not None or out_amax is not None:
             raise ValueError("out_ring and out_amax need out_fmt")
@@ -848,21 +898,24 @@ def mm_act(a, b, sinv_a, sinv_b, act=ACT_NONE, bias=None, aux=None, aux_op=AUX_A
     else:
         if out_ring is None:
             raise ValueError("an FP8 output needs out_ring")
-        _ring_on(out_ring, a, "out_ring")
+        _ring_on(out_ring, dev, "out_ring")
+        _scalar(out_amax, dev, "out_amax")
         kind, dtype = (MM_OUT_E4M3 if out_fmt == E4M3 else MM_OUT_E5M2 if out_fmt == E5M2 else -1), torch.uint8
     if out is None:
-        out = a.new_empty((M, N), dtype=dtype)
+        out = _empty2(M, N, dtype)
     else:
-        _same(out, a, "out", (M, N), dtype)
+        _same(out, dev, "out", (M, N), dtype)
     if z is not None:
-        _same(z, a, "z", (M, N), torch.bfloat16)
+        _same(z, dev, "z", (M, N), torch.bfloat16)
     elif need_z:
-        z = a.new_empty((M, N), dtype=torch.bfloat16)
-    args = CMmActArgs(a.data_ptr(), b.data_ptr(), M, N, K,
-                      (MM_A_E5M2 if fmt_a == E5M2 else 0) | (MM_B_E5M2 if fmt_b == E5M2 else 0), sinv_a.data_ptr(),
-                      1 if na != 1 else 0, sinv_b.data_ptr(), _ptr(bias), act, _ptr(aux), aux_op, _ptr(z), kind,
-                      out.data_ptr(), out_ring.c() if out_ring is not None else _NO_RING, _ptr(out_amax))
-    _check((_LIB or lib()).fp8_mm_act(ctypes.byref(args), _raw_stream(a.get_device())), "fp8_mm_act")
+        z = _empty2(M, N, torch.bfloat16)
+    args = _pack_mm_act(a.data_ptr(), b.data_ptr(), M, N, K,
+                        (MM_A_E5M2 if fmt_a == E5M2 else 0) | (MM_B_E5M2 if fmt_b == E5M2 else 0), sinv_a.data_ptr(),
+                        1 if na != 1 else 0, sinv_b.data_ptr(), _adr(bias), act, _adr(aux), aux_op, _adr(z), kind,
+                        out.data_ptr(), *(_NO_RING if out_ring is None else out_ring._addresses), _adr(out_amax))
+    rc = (_LIB or lib()).fp8_mm_act(args, _raw_stream(dev))
+    if rc:
+        _check(rc, "fp8_mm_act")
     return out, z
 
 
@@ -885,6 +938,9 @@ class ActGrad(NamedTuple):
     dbu: Optional[torch.Tensor]  # float32 [cols], column sums of du
 
 
+_pack_act_bwd = _packer(CActBwdArgs)
+
+
 @_on_stream
 def act_backward(dy, z, act, fmt, ring, u=None, ring_u=None, need_db=False, amax=None, amax_u=None):
     """fp8_act_backward: the gradient of ``mm_act``'s epilogue as FP8 codes.
@@ -897,35 +953,35 @@ def act_backward(dy, z, act, fmt, ring, u=None, ring_u=None, need_db=False, amax
     column sums of dz (and du): the bias gradients.  With ACT_NONE and
     without u, z may be None.  Returns an ActGrad.
     """
-    if dy.dtype not in IN_DTYPE:
-        raise ValueError(f"{dy.dtype} is not one of bfloat16, float16, float32")
-    if dy.dim() != 2 or not dy.is_contiguous():
-        raise ValueError("dy must be a contiguous 2-D tensor")
-    rows, cols = dy.shape
-    _same(z, dy, "z", None, torch.bfloat16)
-    _same(u, dy, "u", None, torch.bfloat16)
+    rows, cols, code = _matrix(dy, "dy")
+    shape, dev = dy.shape, dy.get_device()
+    _same(z, dev, "z", shape, torch.bfloat16)
+    _ring_on(ring, dev, "ring")
+    _scalar(amax, dev, "amax")
     if (u is None) != (ring_u is None):
         raise ValueError("u and ring_u go together")
-    _ring_on(ring, dy, "ring")
-    _ring_on(ring_u, dy, "ring_u")
-    _scalar(amax, dy, "amax")
-    _scalar(amax_u, dy, "amax_u")
+    if u is not None:
+        _same(u, dev, "u", shape, torch.bfloat16)
+        _ring_on(ring_u, dev, "ring_u")
+    _scalar(amax_u, dev, "amax_u")
     L = _LIB or lib()
-    dz = torch.empty_like(dy, dtype=torch.uint8)
-    du = torch.empty_like(dy, dtype=torch.uint8) if u is not None else None
+    dz = _empty2(rows, cols, torch.uint8)
+    du = _empty2(rows, cols, torch.uint8) if u is not None else None
     db = dbu = ws = None
     wsb = 0
     if need_db:
-        db = dy.new_empty(cols, dtype=torch.float32)
+        db = _empty(cols, torch.float32)
         if u is not None:
-            dbu = dy.new_empty(cols, dtype=torch.float32)
+            dbu = _empty(cols, torch.float32)
         wsb = L.fp8_act_backward_workspace_bytes(rows, cols, 0 if u is None else 1)
         if wsb:
-            ws = dy.new_empty(wsb, dtype=torch.uint8)
-    a = CActBwdArgs(dy.data_ptr(), IN_DTYPE[dy.dtype], _ptr(z), _ptr(u), rows, cols, act, fmt, ring.c(),
-                    ring_u.c() if ring_u is not None else _NO_RING, _ptr(amax), _ptr(amax_u), dz.data_ptr(), _ptr(du),
-                    _ptr(db), _ptr(dbu), _ptr(ws), wsb)
-    _check(L.fp8_act_backward(ctypes.byref(a), _raw_stream(dy.get_device())), "fp8_act_backward")
+            ws = _empty(wsb, torch.uint8)
+    args = _pack_act_bwd(dy.data_ptr(), code, _adr(z), _adr(u), rows, cols, act, fmt, *ring._addresses,
+                         *(_NO_RING if ring_u is None else ring_u._addresses), _adr(amax), _adr(amax_u), dz.data_ptr(),
+                         _adr(du), _adr(db), _adr(dbu), _adr(ws), wsb)
+    rc = L.fp8_act_backward(args, _raw_stream(dev))
+    if rc:
+        _check(rc, "fp8_act_backward")
     return ActGrad(dz, du, db, dbu)
 
 

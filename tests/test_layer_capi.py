@@ -131,3 +131,18 @@ def test_mm_act_refusals(L):
                dict(out_kind=1, out_ring=ops.CRing(0x900000, 0x900040, 0x900044, 0x900048, 0x90004C))):
         assert _mm_act(L, **kw) == UNSUP, kw
     assert _mm_act(L, M=0) == ops.FP8_OK
+
+
+def test_packed_arguments_are_the_structures():
+    """The bindings pass packed bytes: every field at its structure's offset."""
+    for cls, pack in ((ops.CNormArgs, ops._pack_norm), (ops.CNormBwdArgs, ops._pack_norm_bwd),
+                      (ops.CMmActArgs, ops._pack_mm_act), (ops.CActBwdArgs, ops._pack_act_bwd)):
+        flat = [f for n, f in cls._fields_ for f in ([ctypes.c_void_p] * 5 if f is ops.CRing else [f])]
+        raw = pack(*range(1, len(flat) + 1))
+        assert len(raw) <= ctypes.sizeof(cls)
+        got = cls.from_buffer_copy(raw + b"\0" * (ctypes.sizeof(cls) - len(raw)))
+        values = []
+        for name, f in cls._fields_:
+            v = getattr(got, name)
+            values += [getattr(v, n) for n, _ in ops.CRing._fields_] if f is ops.CRing else [v]
+        assert values == list(range(1, len(flat) + 1)), cls.__name__
