@@ -148,6 +148,21 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+def _of_buffer(make):
+    """A read-only attribute that is made on first use and kept as long as the ring's buffer is.
+    A view made in inference mode could not be written outside it, so none is made there."""
+    name = make.__name__
+
+    def get(self):
+        v = self._made.get(name)
+        if v is None:
+            with torch.inference_mode(False):
+                v = self._made[name] = make(self)
+        return v
+
+    return property(get, doc=make.__doc__)
+
+
 class Ring:
     """One tensor's delayed-scaling state in a single device buffer.
 
@@ -170,42 +185,44 @@ class Ring:
 
     @buf.setter
     def buf(self, t):
-        # The views and addresses below are made on first use and go with the buffer.
-        self.__dict__.clear()
         self._buf = t
+        self._made = {}
 
     def __getstate__(self):
-        return {"buf": self._buf}
+        state = dict(self.__dict__, buf=self._buf)
+        del state["_buf"], state["_made"]
+        return state
 
     def __setstate__(self, state):
-        self.buf = state["buf"]
+        for name, v in state.items():
+            setattr(self, name, v)
 
-    @functools.cached_property
+    @_of_buffer
     def history(self):
         return self.buf[0:HISTORY_LEN].view(torch.float32)
 
-    @functools.cached_property
+    @_of_buffer
     def idx(self):
         return self.buf[16:17]
 
-    @functools.cached_property
+    @_of_buffer
     def scale(self):
         return self.buf[17:18].view(torch.float32)
 
-    @functools.cached_property
+    @_of_buffer
     def scale_inv(self):
         return self.buf[18:19].view(torch.float32)
 
-    @functools.cached_property
+    @_of_buffer
     def scratch(self):
         return self.buf[20:24]
 
-    @functools.cached_property
+    @_of_buffer
     def _addresses(self):
         base = self.buf.data_ptr()
         return base, base + 16 * 4, base + 17 * 4, base + 18 * 4, base + 20 * 4
 
-    @functools.cached_property
+    @_of_buffer
     def _c(self):
         return CRing(*self._addresses)
 
