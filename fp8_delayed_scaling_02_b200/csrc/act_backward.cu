@@ -322,7 +322,7 @@ extern "C" int fp8_act_backward(const fp8_act_backward_args* p, fp8_stream_t str
   if (some && p->z == nullptr && (gate || p->act != FP8_ACT_NONE)) return FP8_ERR_INVALID_ARG;
   const bool ring_u = p->ring_u.scale != nullptr;
   if (some && gate != ring_u) return FP8_ERR_INVALID_ARG;
-  if (p->amax_out_u != nullptr && !ring_u) return FP8_ERR_INVALID_ARG;
+  if (p->amax_out_u != nullptr && (!ring_u || p->amax_out_u == p->amax_out)) return FP8_ERR_INVALID_ARG;
   if (p->dbu != nullptr && (p->db == nullptr || !ring_u)) return FP8_ERR_INVALID_ARG;
   int rc = ring_check(p->ring, p->amax_out);
   if (rc == FP8_OK && ring_u) rc = ring_check(p->ring_u, p->amax_out_u);

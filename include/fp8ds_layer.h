@@ -187,8 +187,8 @@ int fp8_mm_act(const fp8_mm_act_args* args, fp8_stream_t stream);
  * no initial value; unused without db.  Calls that may overlap need one each.
  * rows, cols >= 0; an empty call still folds amax 0, and sets db to 0.
  * Errors: FP8_ERR_INVALID_ARG (bad enum, negative size, a missing or
- *         superfluous pointer, one ring for both outputs, a workspace that is
- *         missing or too small, an output that overlaps another argument);
+ *         superfluous pointer, one ring or one amax for both outputs, a workspace
+ *         that is missing or too small, an output that overlaps another argument);
  *         FP8_ERR_UNSUPPORTED (an address not aligned to its element, a ring's
  *         scratch not 8-byte aligned, cols above 2^30, rows above 2^31).
  */

@@ -146,3 +146,8 @@ def test_packed_arguments_are_the_structures():
             v = getattr(got, name)
             values += [getattr(v, n) for n, _ in ops.CRing._fields_] if f is ops.CRing else [v]
         assert values == list(range(1, len(flat) + 1)), cls.__name__
+
+
+def test_act_backward_refuses_one_amax_for_both_outputs(L):
+    gate = dict(u=0x300000, ring_u=_ring(0xA00000), duq=0x500000)
+    assert _act_bwd(L, amax_out=0x700000, amax_out_u=0x700000, **gate) == BAD
