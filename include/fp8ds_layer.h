@@ -50,7 +50,7 @@ extern "C" {
  *         without a residual, no output at all, codes without a complete ring
  *         or row_sinv, ring arguments without codes, a ring with row_sinv,
  *         an output that overlaps another argument);
- *         FP8_ERR_UNSUPPORTED (cols above 16384, rows above 2^31, an address
+ *         FP8_ERR_UNSUPPORTED (cols above 16384, rows of 2^31 or more, an address
  *         not aligned to its element, ring.scratch not 8-byte aligned).
  */
 typedef struct {
@@ -190,7 +190,7 @@ int fp8_mm_act(const fp8_mm_act_args* args, fp8_stream_t stream);
  *         superfluous pointer, one ring or one amax for both outputs, a workspace
  *         that is missing or too small, an output that overlaps another argument);
  *         FP8_ERR_UNSUPPORTED (an address not aligned to its element, a ring's
- *         scratch not 8-byte aligned, cols above 2^30, rows above 2^31).
+ *         scratch not 8-byte aligned, cols above 2^30, rows of 2^31 or more).
  */
 typedef struct {
   const void* dy;
