@@ -290,3 +290,26 @@ def test_mm_act_refuses_what_the_binding_can_see():
     with pytest.raises(ops.Fp8Error) as e:
         ops.mm_act(a[:, :24].contiguous(), b[:, :24].contiguous(), sa, sb)
     assert e.value.status == ops.FP8_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("N", [193, 196, 202, 255])
+@pytest.mark.parametrize("out_fmt", [None, ops.E5M2])
+def test_mm_act_odd_pitches_leave_the_neighbours(N, out_fmt):
+    """Rows that start at every alignment, outputs inside larger buffers: nothing beyond them is written."""
+    M, pad = 150, 61  # bases 2 bytes (codes: 1) off the 16-byte grid
+    p = _problem(M, N, 128, N, rows=True)
+    d = {k: p[k].cuda() for k in ("a", "b", "sinv_a", "sinv_b", "bias", "aux")}
+    want, want_z = ops.mm_act(d["a"], d["b"], d["sinv_a"], d["sinv_b"], ops.ACT_SILU, d["bias"], d["aux"], ops.AUX_MUL,
+                              need_z=True, out_fmt=out_fmt, out_ring=None if out_fmt is None else ops.Ring(scale=3.0))
+    dtype = torch.bfloat16 if out_fmt is None else torch.uint8
+    bufs = [torch.full((M * N + 2 * pad,), 7, dtype=t, device="cuda") for t in (dtype, torch.bfloat16, torch.bfloat16)]
+    out, z, aux = (b[pad:pad + M * N].view(M, N) for b in bufs)
+    aux.copy_(d["aux"])
+    if out_fmt is None:
+        out, bufs[0] = aux, bufs[2]  # in place
+    ops.mm_act(d["a"], d["b"], d["sinv_a"], d["sinv_b"], ops.ACT_SILU, d["bias"], aux, ops.AUX_MUL, out_fmt=out_fmt,
+               out_ring=None if out_fmt is None else ops.Ring(scale=3.0), out=out, z=z)
+    assert torch.equal(out, want) and torch.equal(z, want_z)
+    for b in bufs:
+        assert bool((b[:pad] == 7).all()) and bool((b[pad + M * N:] == 7).all())
+    _check(p, ops.ACT_SILU, ops.AUX_MUL, out_fmt)
