@@ -27,7 +27,7 @@ struct SkinnyArgs {
 
 constexpr int kSkinnyMaxM = 32;
 
-bool skinny_wins(int64_t M, int64_t N, int sms);
+bool skinny_wins(int64_t M, int64_t N, int64_t K, int sms);
 int launch_skinny(const SkinnyArgs& a, int sms, cudaStream_t st);  // 1 <= M <= kSkinnyMaxM
 
 }  // namespace fp8ds

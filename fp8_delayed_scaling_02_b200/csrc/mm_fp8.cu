@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "activation.cuh"
+#include "amax_fold.cuh"
 #include "common.cuh"
 #include "fp8_ring.cuh"
 #include "fp8ds_layer.h"
@@ -1406,6 +1407,253 @@ __global__ void __launch_bounds__(ActCfg<BN, PAIR, EPI>::kThreads, 1)
   mm_body<BN, PAIR, EPI>(&tmA, &tmB, &tmC, p, int(blockIdx.x) / PAIR, int(gridDim.x) / PAIR, &tmX, &tmZ);
 }
 
+// ---- K split over a cluster ----------------------------------------------------
+//
+// A few hundred rows of A make fewer tiles than SMs, and each tile's time is its
+// k-blocks' way from L2 into one SM (0.35 us each).  So the CTAs of a cluster
+// share a tile: each sums its part of K into TMEM and puts the float32 sums
+// into its own shared memory, where its operands were; then each takes chunks
+// of 8 columns, adds the parts in the CTAs' order (the same bits in every call)
+// through distributed shared memory, and runs the epilogue on them.  1536 x 4096
+// (N x K) with a residual, whole tiles against split ones: 64 rows 13.4 and 6.5
+// us, 128 rows 13.5 and 7.9, 256 rows 13.6 and 8.9, 512 rows 14.0 and 10.9.
+// What bounds it: the k-blocks that are left (the same rate per SM), and some
+// 5 us that no split shortens: launch, first loads, two cluster barriers, the
+// read of the other CTAs' sums (one epilogue warp per 32 rows instead of four:
+// 512 rows 15.0).
+template <int BN>
+struct SplitCfg {
+  static constexpr int kABytes = kBM * kBK;
+  static constexpr int kStageBytes = kABytes + BN * kBK;
+  static constexpr int kStages = (192 * 1024) / kStageBytes;
+  static constexpr int kParts = 4;  // epilogue warps per 32 rows: a chunk is a chain of latencies
+  static constexpr int kThreads = 32 * (2 + 4 * kParts);
+  static constexpr int kBarOffset = kStages * kStageBytes;
+  static constexpr int kSmemBytes = kBarOffset + 256 + 1024;
+  static_assert(kBM * BN * 4 <= kBarOffset && (2 * kStages + 3) * 8 + 8 <= 256, "shared memory layout");
+};
+
+// Part `rank` of `ranks` of [0, kb).
+__device__ __forceinline__ int split_at(int kb, int rank, int ranks) { return kb * rank / ranks; }
+
+__device__ __forceinline__ float4 ld_cluster16(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <int ACT>
+__device__ __forceinline__ void act8(float (&y)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) act_pair<ACT>(y[j], y[j + 1]);
+}
+
+template <int BN, bool kOut8>
+__global__ void __launch_bounds__(SplitCfg<BN>::kThreads, 1)
+    mm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ MmParams p, const int ranks, const int vec) {
+  using C = SplitCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // the same offset in every CTA
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
+  // bars[0, S) full, [S, 2S) empty, [2S] all products done, [2S + 1] never arrived on
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::kStages + 2);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t bar0 = smem_u32(bars);
+  const uint32_t done_bar = bar0 + 8u * (2 * C::kStages), stall_bar = done_bar + 8u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(cluster_ctarank());
+  const int tile = int(blockIdx.x) / ranks;
+  const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
+  const int kb0 = split_at(p.k_blocks, rank, ranks), kb1 = split_at(p.k_blocks, rank + 1, ranks);
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2 * C::kStages + 2; ++s) mbar_init(bar0 + 8u * s, 1);
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) tmem_alloc_g<1>(smem_u32(tmem_slot), BN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait_prior_grid();
+  const RingArgs ring{p.r_history, p.r_idx, p.r_scale, p.r_scale_inv, p.r_scratch, p.amax_out};
+  RingCache rc{0.0f, 0};
+  if constexpr (kOut8) rc = prefetch_ring(ring);
+  const float s_out = kOut8 ? *p.r_scale : 0.0f;
+  // Epilogue warp: rows, and which of its row's chunks; the first one's operands come early.
+  const int part = (warp - 2) >> 2, row = 32 * (warp & 3) + lane, m = mt * kBM + row;
+  const int c0 = rank + ranks * part;
+  const bool mine = warp >= 2 && m < p.M;
+  uint4 aux0 = make_uint4(0, 0, 0, 0);
+  if (vec && p.aux != nullptr && mine && c0 < BN / 8 && nt * BN + 8 * c0 < p.N)
+    aux0 = *reinterpret_cast<const uint4*>(p.aux + int64_t(m) * p.N + nt * BN + 8 * c0);
+  const float sab = mine ? __fmul_rn(p.sinv_a[p.a_rows ? m : 0], *p.sinv_b) : 0.0f;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int n = 0;  // k-blocks asked for
+      for (; n < kb1 - kb0; ++n) {
+        const int s = n % C::kStages;
+        if (!mbar_wait(bar0 + 8u * (C::kStages + s), ((n / C::kStages) & 1) ^ 1, abort, p.err, kWaitProducerEmpty,
+                       p.wait_ns))
+          break;
+        const uint32_t bar = bar0 + 8u * s, sa = sbase + s * C::kStageBytes;
+        mbar_arrive_expect_tx(bar, C::kStageBytes);
+        tma_load_3d(sa, &tmA, (kb0 + n) * kBK, mt * kBM, 0, bar);
+        tma_load_3d(sa + C::kABytes, &tmB, (kb0 + n) * kBK, nt * BN, 0, bar);
+      }
+      // Every copy has landed before shared memory is released, whoever gave up.
+      for (int i = max(0, n - C::kStages); i < n; ++i) {
+        const unsigned long long t0 = globaltimer_ns();
+        while (!mbar_try_wait(bar0 + 8u * (i % C::kStages), (i / C::kStages) & 1) &&
+               globaltimer_ns() - t0 < kWaitBudgetNs) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int n = 0; n < kb1 - kb0; ++n) {
+        const int s = n % C::kStages;
+        if (!mbar_wait(bar0 + 8u * s, (n / C::kStages) & 1, abort, p.err, kWaitMmaFull, p.wait_ns)) break;
+        tc_fence_after();
+        const uint64_t ad = sdesc_k128(sbase + s * C::kStageBytes);
+        const uint64_t bd = sdesc_k128(sbase + s * C::kStageBytes + C::kABytes);
+#pragma unroll
+        for (int k = 0; k < kBK / kUmmaK; ++k)
+          umma_f8(tmem_base, ad + 2u * k, bd + 2u * k, p.idesc, (n != 0 || k != 0) ? 1u : 0u);
+        umma_commit(bar0 + 8u * (C::kStages + s));
+      }
+      // Also after a wait that gave up: TMEM is released behind every product.
+      umma_commit(done_bar);
+      const unsigned long long t0 = globaltimer_ns();
+      while (!mbar_try_wait(done_bar, 0) && globaltimer_ns() - t0 < kWaitBudgetNs) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // (Testing: with the stall site set here, the wait is on a barrier that
+    // nothing completes, so it runs out and the abort path runs.)
+    const bool stall = p.stall == kWaitEpilogueTmemFull;
+    bool ok = mbar_wait(stall ? stall_bar : done_bar, 0, abort, p.err, kWaitEpilogueTmemFull, p.wait_ns);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (ok && mt * kBM + 32 * (warp & 3) < p.M) {  // float4 c of row r at (128 c + r) * 16
+      tc_fence_after();
+#pragma unroll
+      for (int h = part; h < BN / 16; h += C::kParts) {
+        uint32_t r[16];
+        tmem_ld16_nowait(tmem_base + (uint32_t(32 * (warp & 3)) << 16) + uint32_t(16 * h), r);
+        tmem_wait_ld16(r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          st_shared16(sbase + uint32_t((4 * h + j) * kBM + row) * 16u, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+  }
+  cluster_sync();
+  float amax = 0.0f;
+  if (mine && !*abort) {
+    for (int c = c0; c < BN / 8; c += ranks * C::kParts) {
+      const int n0 = nt * BN + 8 * c;
+      if (n0 >= p.N) break;
+      const int64_t at = int64_t(m) * p.N + n0;
+      const int cols = min(8, p.N - n0);
+      float x[8], y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
+      if (p.aux != nullptr) {
+        if (vec) {
+          const uint4 v = c == c0 ? aux0 : *reinterpret_cast<const uint4*>(p.aux + at);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < cols) x[j] = __uint_as_float(uint32_t(p.aux[at + j]) << 16);
+        }
+      }
+      const uint32_t here = sbase + uint32_t(2 * c * kBM + row) * 16u;
+#pragma unroll 4
+      for (int k = 0; k < ranks; ++k) {
+        const uint32_t there = mapa_shared(here, uint32_t(k));
+        const float4 lo = ld_cluster16(there), hi = ld_cluster16(there + kBM * 16u);
+        add2(y[0], y[1], lo.x, lo.y);
+        add2(y[2], y[3], lo.z, lo.w);
+        add2(y[4], y[5], hi.x, hi.y);
+        add2(y[6], y[7], hi.z, hi.w);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float b = p.bias != nullptr && j < cols ? __ldg(p.bias + n0 + j) : 0.0f;
+        y[j] = j < cols ? fmaf(y[j], sab, b) : 0.0f;
+      }
+      auto store_bf16 = [&](uint16_t* o) {
+        if (vec) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          *reinterpret_cast<uint4*>(o + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < cols) o[at + j] = __bfloat16_as_ushort(__float2bfloat16_rn(y[j]));
+        }
+      };
+      if (p.z != nullptr) store_bf16(p.z);
+      switch (p.act) {  // uniform
+        case FP8_ACT_RELU: act8<FP8_ACT_RELU>(y); break;
+        case FP8_ACT_GELU: act8<FP8_ACT_GELU>(y); break;
+        case FP8_ACT_SILU: act8<FP8_ACT_SILU>(y); break;
+        default: break;
+      }
+      if (p.aux != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = p.aux_mul ? __fmul_rn(y[j], x[j]) : __fadd_rn(y[j], x[j]);
+      }
+      if constexpr (kOut8) {
+        uint32_t w[2];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));  // 0 beyond the last column
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          w[j] = p.out_fmt == FP8_E5M2 ? cvt4<FP8_E5M2>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out)
+                                       : cvt4<FP8_E4M3>(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], s_out);
+        if (vec) {
+          *reinterpret_cast<uint2*>(p.out8 + at) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < cols) p.out8[at + j] = uint8_t(w[j >> 2] >> (8 * (j & 3)));
+        }
+      } else {
+        store_bf16(p.out);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // nobody reads this CTA's shared memory any more
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_g<1>(tmem_base, BN);
+  if constexpr (kOut8) {
+    if (p.out_fmt == FP8_E5M2) amax_ticket_fold<FP8_E5M2, C::kThreads>(amax, ring, s_out, rc, gridDim.x);
+    else amax_ticket_fold<FP8_E4M3, C::kThreads>(amax, ring, s_out, rc, gridDim.x);
+  }
+}
+
 // Two independent GEMMs in one persistent launch (the dX and dW GEMMs of a
 // linear's backward): CTAs (pairs) [0, split) work on problem 0 and the rest
 // on problem 1, each set over its own tiles, so a problem with too few tiles
@@ -1763,6 +2011,98 @@ int launch_act(const MmProblem& q, const MmChoice& c, cudaStream_t st) {
   if (out8) return launch_act_epi<BN, PAIR, kEpiAct | kEpiOut8>(q, c, st);
   return q.p.z != nullptr ? launch_act_epi<BN, PAIR, kEpiAct | kEpiZ>(q, c, st)
                           : launch_act_epi<BN, PAIR, kEpiAct>(q, c, st);
+}
+
+constexpr double kSplitJoin = 1.9;
+template <int BN, bool kOut8>
+bool ensure_split_attr(int dev) {
+  static bool done[64] = {false};
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(mm_split_kernel<BN, kOut8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             SplitCfg<BN>::kSmemBytes) != cudaSuccess)
+      return false;
+    done[dev] = true;
+  }
+  return true;
+}
+
+constexpr int kMaxRanks = 8;  // CTAs of a cluster that every device takes
+
+// Clusters of `ranks` CTAs, one to an SM, that can be resident at once.
+int max_clusters(int ranks) {
+  static int cached[64][kMaxRanks + 1] = {{0}};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || !ensure_split_attr<64, false>(dev)) return 0;
+  int& n = cached[dev][ranks];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranks);
+    cfg.blockDim = dim3(SplitCfg<64>::kThreads);
+    cfg.dynamicSmemBytes = SplitCfg<64>::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int k = 0;
+    if (cudaOccupancyMaxActiveClusters(&k, mm_split_kernel<64, false>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    n = k;
+  }
+  return n;
+}
+
+// CTAs per cluster and tile width of the K split, or 0 where whole tiles are
+// modelled to take no longer: `whole` us.  A split launch takes what a whole one
+// of the same tile width does, but for its share of the k-blocks, and the join:
+// 1.9 us puts the border where they take the same (4096 x 1536: 256 rows 8.2 us
+// either way, 128 rows 8.0 whole and 7.3 split; 1536 x 1024, 200 rows: 6.2 and 6.3).
+struct SplitChoice {
+  int bn, ranks;
+};
+
+SplitChoice choose_split(int64_t M, int64_t N, int64_t K, double whole) {
+  const int64_t kb = (K + kBK - 1) / kBK;
+  SplitChoice best{0, 0};
+  for (int bn = 64; bn <= 128; bn *= 2) {
+    const int64_t tiles = ((M + kBM - 1) / kBM) * ((N + bn - 1) / bn);
+    for (int ranks = 2; ranks <= kMaxRanks && ranks <= kb; ++ranks) {
+      const double us =
+          (bn == 64 ? 3.3 : 3.5) + kSplitJoin + double((kb + ranks - 1) / ranks) * (bn == 64 ? 0.35 : 0.37);
+      if (us >= whole || tiles > max_clusters(ranks)) continue;
+      whole = us;
+      best = SplitChoice{bn, ranks};
+    }
+  }
+  return best;
+}
+
+template <int BN, bool kOut8>
+int launch_split1(const MmProblem& q, int ranks, cudaStream_t st) {
+  CUtensorMap ta, tb, tc;
+  MmParams p = q.p;
+  p.tma_store = 0;  // no map of the output
+  const MmChoice c{BN, 1, 0, 0, 0, 0, 0.0};
+  const int rc = prepare_mm<BN, 1>(q.A, q.B, q.M, q.N, q.K, 1, nullptr, p, c, nullptr, ta, tb, tc);
+  if (rc != FP8_OK) return rc;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || !ensure_split_attr<BN, kOut8>(dev))
+    return FP8_ERR_CUDA;
+  const int vec = q.N % 8 == 0 && on(p.aux, 16) && on(p.z, 16) && on(p.out, 16) && on(p.out8, 8);
+  return launch_pdl(mm_split_kernel<BN, kOut8>, dim3(unsigned(p.tiles_total) * ranks), dim3(SplitCfg<BN>::kThreads),
+                    SplitCfg<BN>::kSmemBytes, st, ranks, ta, tb, p, ranks, vec) == cudaSuccess
+             ? FP8_OK
+             : FP8_ERR_CUDA;
+}
+
+int launch_split(const MmProblem& q, const SplitChoice& c, cudaStream_t st) {
+  const bool out8 = (q.epi & kEpiOut8) != 0;
+  if (c.bn == 64) return out8 ? launch_split1<64, true>(q, c.ranks, st) : launch_split1<64, false>(q, c.ranks, st);
+  return out8 ? launch_split1<128, true>(q, c.ranks, st) : launch_split1<128, false>(q, c.ranks, st);
 }
 
 template <int BN, int PAIR>
@@ -2154,7 +2494,7 @@ extern "C" int fp8_mm_act(const fp8_mm_act_args* a, fp8_stream_t stream) {
                                                                                                  : FP8_ERR_CUDA;
   const int sms = sm_count();
   if (sms <= 0) return FP8_ERR_CUDA;
-  if (skinny_wins(q.M, q.N, sms)) {
+  if (skinny_wins(q.M, q.N, q.K, sms)) {
     SkinnyArgs s{a->A, a->B, p.M, p.N, p.K, a->layout & FP8_MM_A_E5M2 ? FP8_E5M2 : FP8_E4M3,
                  a->layout & FP8_MM_B_E5M2 ? FP8_E5M2 : FP8_E4M3, a->sinv_a, p.a_rows, a->sinv_b, a->bias, p.act, p.aux,
                  p.aux_mul, p.z, p.out, p.out8, p.out_fmt, RingArgs{}};
@@ -2164,6 +2504,8 @@ extern "C" int fp8_mm_act(const fp8_mm_act_args* a, fp8_stream_t stream) {
     return launch_skinny(s, sms, st);
   }
   const MmChoice c = choose_mm(q.M, q.N, q.K, 1, sms, false, 0);
+  const SplitChoice sp = choose_split(q.M, q.N, q.K, c.cost);
+  if (sp.ranks > 0) return launch_split(q, sp, st);
   if (c.pair == 2) return launch_act<256, 2>(q, c, st);
   if (c.bn == 256) return launch_act<256, 1>(q, c, st);
   if (c.bn == 128) return launch_act<128, 1>(q, c, st);

@@ -161,12 +161,13 @@ cudaError_t launch_fmt(const SkinnyArgs& a, int sms, cudaStream_t st) {
 }  // namespace
 
 // The FP8 mma of mma.sync converts its operands first, at a rate that more
-// tokens soon reach.  Against the tile kernel, at N x K of 1536 x 4096, 4096 x
-// 1536, 4096 x 4096 and 8192 x 4096 (us here / there): 8 tokens 4.8 / 13.9, 3.4 /
-// 8.0, 5.4 / 14.2, 8.5 / 18.7; 16 tokens 6.4 / 13.9, 4.1 / 7.9, 6.7 / 14.2, 15.1 /
-// 18.1; 32 tokens 10.4 / 13.9, 6.5 / 7.9, 11.1 / 14.1, 33.7 / 15.0.
-bool skinny_wins(int64_t M, int64_t N, int sms) {
-  return M <= 16 || (M <= kSkinnyMaxM && (N + 15) / 16 <= 2 * int64_t(sms));
+// tokens and longer rows soon reach.  Against the tile kernels, with the K split
+// where it is taken, at N x K of 1536 x 4096, 4096 x 1536, 4096 x 4096, 8192 x 4096
+// and 512 x 512 (us here / there): 8 tokens 4.7 / 5.8, 3.2 / 6.2, 5.2 / 7.8, 8.5 /
+// 13.1, 2.1 / 4.6; 16 tokens 6.5 / 5.8, 4.1 / 6.0, 6.9 / 7.8, 14.9 / 13.4, 2.5 /
+// 4.6; 24 tokens 9.4 / 6.0, 6.1 / 6.1, 10.3 / 8.1, - / 13.4, 3.3 / 4.6.
+bool skinny_wins(int64_t M, int64_t N, int64_t K, int sms) {
+  return M <= 16 || (M <= kSkinnyMaxM && K <= 1536 && (N + 15) / 16 <= 2 * int64_t(sms));
 }
 
 int launch_skinny(const SkinnyArgs& a, int sms, cudaStream_t st) {

@@ -135,9 +135,11 @@ typedef enum { FP8_AUX_ADD = 0, FP8_AUX_MUL = 1 } fp8_aux_op;
  * bias    float32 [N] or NULL.  aux: bf16 [M, N] or NULL.  All contiguous.
  *         out may be aux itself (a residual stream updated in place).
  * M, N >= 0, K >= 0 with K % 16 == 0; K == 0 gives z = bias; an empty output
- * still folds amax 0.  A few rows of A (16, or 32 with few columns) take a
- * kernel that reads B once, straight into registers; its sums run in another
- * order than the tile kernel's, within the same bound.
+ * still folds amax 0.  A few rows of A (16, or 32 with few columns and short
+ * K) take a kernel that reads B once, straight into registers; a few hundred
+ * rows, whose tiles leave SMs idle, share each tile's K among the CTAs of a
+ * cluster.  Their sums run in other orders than the whole-tile kernel's, within
+ * the same bound; the order depends on the sizes and the device only.
  * Errors as fp8_mm_ex; FP8_ERR_INVALID_ARG also for an unknown act or aux_op,
  *         other layout bits, an output that overlaps another argument;
  *         FP8_ERR_UNSUPPORTED for an address not aligned to its element.

@@ -313,3 +313,43 @@ def test_mm_act_odd_pitches_leave_the_neighbours(N, out_fmt):
     for b in bufs:
         assert bool((b[:pad] == 7).all()) and bool((b[pad + M * N:] == 7).all())
     _check(p, ops.ACT_SILU, ops.AUX_MUL, out_fmt)
+
+
+# Few tiles and long K: the CTAs of a cluster share a tile's K, in equal and unequal parts.
+@pytest.mark.parametrize("M,N,K", [(33, 64, 4096), (24, 512, 4096), (64, 1536, 4096), (100, 1000, 4096), (129, 1537, 4000),
+                                   (256, 1536, 4096), (512, 1536, 4096), (65, 130, 16000), (40, 8, 2048), (128, 4096, 1536),
+                                   (48, 520, 1040), (100, 96, 656)])
+def test_mm_act_few_tiles_and_long_k(M, N, K):
+    for k, (act, aux, out_fmt) in enumerate(((ops.ACT_SILU, ops.AUX_MUL, ops.E4M3), (ops.ACT_GELU, ops.AUX_ADD, None),
+                                             (ops.ACT_RELU, None, ops.E5M2))):
+        p = _problem(M, N, K, 31 * M + k, rows=k == 0, bias=k != 1, aux=aux is not None)
+        _check(p, act, aux or ops.AUX_ADD, out_fmt)
+        runs = [_run(p, act, aux or ops.AUX_ADD, out_fmt, None if out_fmt is None else ops.Ring(scale=3.0)) for _ in range(3)]
+        for out, z in runs[1:]:  # the same bits in every call
+            assert torch.equal(out, runs[0][0]) and torch.equal(z, runs[0][1])
+
+
+def test_mm_act_few_tiles_twice_at_a_time_and_captured():
+    p = _problem(96, 1536, 4096, 77, rows=True)
+    want = _run(p, ops.ACT_SILU, ops.AUX_MUL, ops.E4M3, ops.Ring(scale=3.0))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(20):
+        for s, o in zip(streams, outs):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                o.append(_run(p, ops.ACT_SILU, ops.AUX_MUL, ops.E4M3, ops.Ring(scale=3.0)))
+    torch.cuda.synchronize()
+    for o in outs:
+        for out, z in o:
+            assert torch.equal(out, want[0]) and torch.equal(z, want[1])
+    d = {k: p[k].cuda() for k in ("a", "b", "sinv_a", "sinv_b", "bias", "aux")}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, z = ops.mm_act(d["a"], d["b"], d["sinv_a"], d["sinv_b"], ops.ACT_SILU, d["bias"], d["aux"], ops.AUX_MUL,
+                            need_z=True)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(z, want[1])
