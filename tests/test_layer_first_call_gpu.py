@@ -46,3 +46,29 @@ def test_a_captured_call_may_be_the_first(M):
     require_gpu()
     r = subprocess.run([sys.executable, "-c", PROGRAM, ROOT, str(M)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+SPLIT_PROGRAM = """
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+from fp8_delayed_scaling_02_b200 import ops
+g = torch.Generator().manual_seed(0)
+a, b = ((torch.randn(n, 4096, generator=g) / 8).to(torch.float8_e4m3fn).view(torch.uint8).cuda() for n in (64, 512))
+one = torch.ones(1, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = ops.mm_act(a, b, one, one, ops.ACT_GELU, need_z=True)
+graph.replay()
+want = ops.mm_act(a, b, one, one, ops.ACT_GELU, need_z=True)
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(got, want))
+print("captured")
+"""
+
+
+def test_a_captured_product_with_a_split_k_may_be_the_first():
+    require_gpu()
+    r = subprocess.run([sys.executable, "-c", SPLIT_PROGRAM, ROOT], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

@@ -146,7 +146,8 @@ def test_mm_act_offsets_beyond_31_bits(out_fmt, N):
     assert torch.equal(out[last:], want[:M - last])
 
 
-@pytest.mark.parametrize("M,N,aux", [(128, 256, False), (128, 256, True), (600, 1024, True), (600, 1000, True)])
+@pytest.mark.parametrize("M,N,aux", [(128, 256, False), (128, 256, True), (600, 1024, True), (600, 1000, True),
+                                     (2000, 1024, True), (2000, 1000, True)])
 def test_mm_act_wait_runs_out_then_the_next_call_is_right(M, N, aux):
     """The timeout path (see the timeout tests of the product): the stopped kernel lets its
     operand loads land, frees what it holds and returns; the next call is whole."""
