@@ -125,7 +125,8 @@ WaitCfg wait_cfg() {
 
 extern "C" int fp8_debug_wait(uint64_t budget_ns, uint32_t stall_site) {
   if (budget_ns == 0 || budget_ns > fp8ds::kWaitBudgetNs) return FP8_ERR_INVALID_ARG;
-  if (stall_site != 0 && stall_site != fp8ds::kWaitEpilogueTmemFull && stall_site != fp8ds::kWaitQuantizeTma)
+  if (stall_site != 0 && stall_site != fp8ds::kWaitEpilogueTmemFull && stall_site != fp8ds::kWaitQuantizeTma &&
+      stall_site != fp8ds::kWaitSplitOneCta)
     return FP8_ERR_INVALID_ARG;
   fp8ds::g_wait_budget_ns.store(budget_ns, std::memory_order_relaxed);
   fp8ds::g_stall_site.store(stall_site, std::memory_order_relaxed);

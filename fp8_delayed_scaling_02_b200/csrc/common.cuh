@@ -29,6 +29,7 @@ enum WaitSite : uint32_t {
   kWaitQuantizeTma = 6,
   kWaitSplitK = 7,
   kWaitEpilogueAux = 8,
+  kWaitSplitOneCta = 9,  // kWaitEpilogueTmemFull, stalled in the first CTA of each cluster alone
 };
 
 // Library-global device error word (defined in capi.cu, relocatable device code

@@ -1443,6 +1443,12 @@ __device__ __forceinline__ float4 ld_cluster16(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 template <int ACT>
 __device__ __forceinline__ void act8(float (&y)[8]) {
 #pragma unroll
@@ -1542,7 +1548,7 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, 1)
   } else {
     // (Testing: with the stall site set here, the wait is on a barrier that
     // nothing completes, so it runs out and the abort path runs.)
-    const bool stall = p.stall == kWaitEpilogueTmemFull;
+    const bool stall = p.stall == kWaitEpilogueTmemFull || (p.stall == kWaitSplitOneCta && rank == 0);
     bool ok = mbar_wait(stall ? stall_bar : done_bar, 0, abort, p.err, kWaitEpilogueTmemFull, p.wait_ns);
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (ok && mt * kBM + 32 * (warp & 3) < p.M) {  // float4 c of row r at (128 c + r) * 16
@@ -1561,8 +1567,12 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, 1)
     __syncwarp();
   }
   cluster_sync();
+  // A CTA that gave up has no sums: the others of its cluster must not join
+  // what lies in their place.
+  const uint32_t flag = lane < ranks ? ld_cluster(mapa_shared(smem_u32(tmem_slot + 1), uint32_t(lane))) : 0u;
+  const bool gave_up = __any_sync(0xFFFFFFFFu, flag != 0u);
   float amax = 0.0f;
-  if (mine && !*abort) {
+  if (mine && !gave_up) {
     for (int c = c0; c < BN / 8; c += ranks * C::kParts) {
       const int n0 = nt * BN + 8 * c;
       if (n0 >= p.N) break;

@@ -1005,6 +1005,7 @@ def act_backward(dy, z, act, fmt, ring, u=None, ring_u=None, need_db=False, amax
 WAIT_BUDGET_DEFAULT_NS = 2_000_000_000
 SITE_EPILOGUE_TMEM_FULL = 4   # fp8_mm: the epilogue's wait for an accumulator
 SITE_QUANTIZE_TMA = 6         # fp8_quantize: the producer / consumer waits
+SITE_SPLIT_ONE_CTA = 9        # fp8_mm_act with a split K: site 4 in one CTA of each cluster
 
 
 def debug_wait(budget_ns=WAIT_BUDGET_DEFAULT_NS, stall_site=0):

@@ -532,9 +532,11 @@ int fp8_device_info(int* sm_count, const char** arch);
  *                    tile kernels, 16-byte aligned or element-aligned base):
  *                    the consumers' wait for a staged input tile.  The row
  *                    layout's kernel and the transposed / dual kernel of
- *                    other row widths (plain loads) have no waits to shorten.
- * A wait that runs out records its site code in the device error word
- * (fp8_device_error), the kernel stops early and returns; its outputs are
+ *                    other row widths (plain loads) have no waits to shorten;
+ *                 9  fp8_mm_act where the CTAs of a cluster share a tile's K:
+ *                    as 4, in the first CTA of each cluster alone.
+ * A wait that runs out records its site code (9: that of 4) in the device
+ * error word (fp8_device_error), the kernel stops early and returns; its outputs are
  * undefined and the ring of a stalled quantize has folded an amax of 0.
  * Restore the defaults with fp8_debug_wait(2000000000, 0).
  * Errors: FP8_ERR_INVALID_ARG for a budget of 0 or above 2e9, or another site.
