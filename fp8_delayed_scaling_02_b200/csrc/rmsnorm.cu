@@ -15,7 +15,7 @@
 //   * groups walk over the rows of one wave of resident blocks;
 //   * dgamma: partial sums per thread, then each block adds its groups' in
 //     order and writes one float32 row; a second launch adds those rows, in
-//     order, so every bit depends on the sizes and the device only.
+//     order, so every bit depends on the sizes, the type and the device only.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -377,12 +377,15 @@ RowSplit split_fwd(int64_t cols, int bytes) {
 
 // Backward: one vector per thread while a row's warps fit a block, for the
 // dgamma sums and the second pass need the registers, and one large block per
-// SM, so that there are few rows of partial sums.
-constexpr int bwd_threads(int bytes, bool aligned, int v) { return bytes == 2 && aligned && v == 1 ? 768 : 512; }
+// SM, so that there are few rows of partial sums: 768 threads of 16-bit values
+// take 8192 x 1536 in 23.2 us, 512 threads in 37.6 (and 8192 x 1537, whose loads
+// spill 12 bytes at 768, in 62.6 and 84.8).  Not by the alignment: which rows a
+// thread adds, and so every bit of dgamma, depends on the sizes and the type.
+constexpr int bwd_threads(int bytes, int v) { return bytes == 2 && v == 1 ? 768 : 512; }
 
-RowSplit split_bwd(int64_t cols, int bytes, bool aligned) {
+RowSplit split_bwd(int64_t cols, int bytes) {
   const int v = cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4;
-  return split_at(cols, v, bwd_threads(bytes, aligned, v) / 32);
+  return split_at(cols, v, bwd_threads(bytes, v) / 32);
 }
 
 int norm_shape_check(int dtype, int64_t rows, int64_t cols) {
@@ -426,7 +429,7 @@ template <int DT, bool kAligned, int V>
 int launch_bwd1(const NormBwdArgs& a, const RowSplit& s, int64_t grid, cudaStream_t st) {
   // Shared sums of several groups: at most 8192 columns, since more leave one group.
   const size_t smem = s.groups > 1 ? size_t((a.cols + 7) & ~7) * 4 : 0;
-  const cudaError_t e = launch_pdl(rmsnorm_bwd_kernel<DT, kAligned, V, bwd_threads(In<DT>::kBytes, kAligned, V)>,
+  const cudaError_t e = launch_pdl(rmsnorm_bwd_kernel<DT, kAligned, V, bwd_threads(In<DT>::kBytes, V)>,
                                    dim3(unsigned(grid)), dim3(s.threads()), smem, st, 1, a);
   return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
@@ -545,7 +548,7 @@ extern "C" int fp8_rmsnorm_backward(const fp8_rmsnorm_backward_args* p, fp8_stre
   if (sms <= 0) return FP8_ERR_CUDA;
   const bool al = p->cols % 8 == 0 && on(p->dy, 16) && on(p->h, 16) && on(p->dres, 16) && on(p->dx, 16) &&
                   on(p->gamma, 16);
-  RowSplit s = split_bwd(p->cols, eb, al);
+  RowSplit s = split_bwd(p->cols, eb);
   s.groups = int(std::max<int64_t>(1, std::min<int64_t>(s.groups, (p->rows + sms - 1) / sms)));  // few rows: all SMs
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((p->rows + s.groups - 1) / s.groups, sms));
   NormBwdArgs a{};

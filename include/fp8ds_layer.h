@@ -79,8 +79,8 @@ int fp8_rmsnorm(const fp8_rmsnorm_args* args, fp8_stream_t stream);
  *            the gradient of x and, the same values, of residual.  dres is the
  *            gradient that reaches h past the norm (NULL: none).
  *   dgamma = sum over rows of dy * n, float32 [cols] (NULL: not wanted).  The
- *            order of the sums depends on rows, cols and the device only, so
- *            repeated calls give the same bits.
+ *            order of the sums depends on rows, cols, dtype and the device only, so
+ *            repeated calls give the same bits, whatever the addresses.
  * dy, h, dres, dx  [rows, cols], contiguous, element type dtype; dx may be dy
  *         or dres itself.
  * workspace  at least fp8_rmsnorm_backward_workspace_bytes(rows, cols) bytes,
@@ -184,7 +184,7 @@ int fp8_mm_act(const fp8_mm_act_args* args, fp8_stream_t stream);
  *         saved, and the operand it multiplied by.  With FP8_ACT_NONE and no
  *         u, z may be NULL: a cast of dy that also gives the bias gradient.
  * The sums' order depends on rows, cols and the device only: repeated calls
- * give the same bits.  workspace: at least
+ * give the same bits, whatever the addresses.  workspace: at least
  * fp8_act_backward_workspace_bytes(rows, cols, gated) bytes, 4-byte aligned,
  * no initial value; unused without db.  Calls that may overlap need one each.
  * rows, cols >= 0; an empty call still folds amax 0, and sets db to 0.
