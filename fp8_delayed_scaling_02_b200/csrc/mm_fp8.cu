@@ -718,9 +718,10 @@ __device__ __forceinline__ float act_epilogue(const CUtensorMap* tmC, const CUte
     // (Testing: with the stall site set here, the wait is on a barrier that
     // nothing completes, so it runs out and the abort path runs.)
     const bool stall = p.stall == kWaitEpilogueTmemFull;
-    if (!mbar_wait(stall ? stall_bar : tfull0 + 8u * acc, stall ? 0u : (i >> 1) & 1, abort, p.err,
-                   kWaitEpilogueTmemFull, p.wait_ns))
-      break;
+    bool ok = mbar_wait(stall ? stall_bar : tfull0 + 8u * acc, stall ? 0u : (i >> 1) & 1, abort, p.err,
+                        kWaitEpilogueTmemFull, p.wait_ns);
+    ok = __all_sync(0xFFFFFFFFu, ok);  // lanes give up each by its own clock; the warp stays whole
+    if (!ok) break;
     tc_fence_after();
     __syncwarp();
     const uint32_t tbase = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + part * 64);
@@ -1088,9 +1089,10 @@ __device__ __forceinline__ void mm_body(const CUtensorMap* tmA, const CUtensorMa
       // (Testing: with the stall site set here, the wait is on a barrier that
       // nothing completes, so it runs out and the abort path runs.)
       const bool stall = p.stall == kWaitEpilogueTmemFull;
-      if (!mbar_wait(stall ? stall_bar : tfull_bar(acc), stall ? 0u : acc_par, abort, p.err, kWaitEpilogueTmemFull,
-                     p.wait_ns))
-        break;
+      bool ok = mbar_wait(stall ? stall_bar : tfull_bar(acc), stall ? 0u : acc_par, abort, p.err,
+                          kWaitEpilogueTmemFull, p.wait_ns);
+      ok = __all_sync(0xFFFFFFFFu, ok);  // lanes give up each by its own clock; the warp stays whole
+      if (!ok) break;
       tc_fence_after();
       int b, mt, nt;
       decode_tile(p, t, b, mt, nt);
