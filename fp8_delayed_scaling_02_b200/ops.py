@@ -8,6 +8,7 @@ device memory and the current stream.
 
 import ctypes
 import functools
+import inspect
 import os
 import struct
 from typing import NamedTuple, Optional
@@ -680,9 +681,17 @@ def _packer(cls):
 def _on_stream(fn):
     """Runs ``fn`` with ``stream`` (default: the current one) and its first tensor's device
     current, so that what it allocates and launches belongs to that stream."""
+    params = list(inspect.signature(fn).parameters.values())
+    first = params[0].name
 
     @functools.wraps(fn)
-    def call(x, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        if args:
+            x, args = args[0], args[1:]
+        elif first in kw:
+            x = kw.pop(first)
+        else:
+            raise TypeError(f"{fn.__name__}() missing 1 required argument: '{first}'")
         dev = x.get_device()
         if dev < 0:
             raise ValueError("the tensors must be CUDA tensors")
@@ -693,6 +702,8 @@ def _on_stream(fn):
         with torch.cuda.device(x.device), torch.cuda.stream(stream):
             return fn(x, *args, **kw)
 
+    call.__signature__ = inspect.Signature([*params, inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY,
+                                                                       default=None)])
     return call
 
 
