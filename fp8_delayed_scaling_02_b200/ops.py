@@ -150,15 +150,19 @@ def _ptr(t):
 
 
 def _of_buffer(make):
-    """A read-only attribute that is made on first use and kept as long as the ring's buffer is.
-    A view made in inference mode could not be written outside it, so none is made there."""
+    """A read-only attribute that is made on first use and kept as long as the ring's buffer is,
+    and stays where it is.  A view made in inference mode could not be written outside it, so
+    none is made there."""
     name = make.__name__
 
     def get(self):
-        v = self._made.get(name)
-        if v is None:
-            with torch.inference_mode(False):
-                v = self._made[name] = make(self)
+        at = self._at()
+        made = self._made.get(name)
+        if made is not None and made[0] == at:  # else new, or buf.data = ..., buf.set_(...)
+            return made[1]
+        with torch.inference_mode(False):
+            v = make(self)
+        self._made[name] = at, v
         return v
 
     return property(get, doc=make.__doc__)
@@ -187,11 +191,12 @@ class Ring:
     @buf.setter
     def buf(self, t):
         self._buf = t
+        self._at = t.data_ptr
         self._made = {}
 
     def __getstate__(self):
         state = dict(self.__dict__, buf=self._buf)
-        del state["_buf"], state["_made"]
+        del state["_buf"], state["_at"], state["_made"]
         return state
 
     def __setstate__(self, state):
