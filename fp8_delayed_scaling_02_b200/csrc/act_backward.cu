@@ -327,11 +327,13 @@ extern "C" int fp8_act_backward(const fp8_act_backward_args* p, fp8_stream_t str
   int rc = ring_check(p->ring, p->amax_out);
   if (rc == FP8_OK && ring_u) rc = ring_check(p->ring_u, p->amax_out_u);
   if (rc == FP8_ERR_INVALID_ARG) return rc;
-  if (ring_u && p->ring.scratch == p->ring_u.scratch) return FP8_ERR_INVALID_ARG;
+  const RingWords words(p->ring, p->amax_out), words_u(ring_u ? p->ring_u : fp8_ring{}, p->amax_out_u);
+  if (words.clash(words_u)) return FP8_ERR_INVALID_ARG;
   if (rc != FP8_OK) return rc;
   if (p->cols > (int64_t(1) << 30) || p->rows > INT32_MAX) return FP8_ERR_UNSUPPORTED;
   const int eb = p->dtype == FP8_IN_FP32 ? 4 : 2;
-  if (!on(p->dy, eb) || !on(p->z, 2) || !on(p->u, 2) || !on(p->db, 4) || !on(p->dbu, 4) || !on(p->workspace, 4))
+  if (!on(p->dy, eb) || !on(p->z, 2) || !on(p->u, 2) || !on(p->db, 4) || !on(p->dbu, 4) || !on(p->workspace, 4) ||
+      !words.aligned() || !words_u.aligned())
     return FP8_ERR_UNSUPPORTED;
   const size_t n = size_t(p->rows) * size_t(p->cols);
   const Span spans[] = {{p->dy, n * eb, false, false, false},
@@ -342,7 +344,7 @@ extern "C" int fp8_act_backward(const fp8_act_backward_args* p, fp8_stream_t str
                         {p->db, size_t(p->cols) * 4, true, false, false},
                         {p->dbu, size_t(p->cols) * 4, true, false, false},
                         {p->workspace, p->db ? p->workspace_bytes : 0, true, false, false}};
-  if (spans_clash(spans, 8)) return FP8_ERR_INVALID_ARG;
+  if (spans_clash(spans, 8) || words.clash(spans, 8) || words_u.clash(spans, 8)) return FP8_ERR_INVALID_ARG;
   const int sms = sm_count_current();
   if (sms <= 0) return FP8_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

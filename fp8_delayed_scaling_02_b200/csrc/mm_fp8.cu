@@ -2479,18 +2479,22 @@ extern "C" int fp8_mm_act(const fp8_mm_act_args* a, fp8_stream_t stream) {
   const int rc = mm_validate(a->A, a->B, a->M, a->N, a->K, 1, nullptr, a->layout, a->sinv_a, a->sinv_b, a->bias,
                              out8 ? nullptr : static_cast<uint16_t*>(a->out), q, &ex);
   if (rc != FP8_OK) return rc;
-  if (!on(a->aux, 2) || !on(a->z, 2) || !on(a->sinv_a, 4) || !on(a->sinv_b, 4) || !on(a->bias, 4))
+  const RingWords words(out8 ? a->out_ring : fp8_ring{}, a->out_amax);
+  if (!on(a->aux, 2) || !on(a->z, 2) || !on(a->sinv_a, 4) || !on(a->sinv_b, 4) || !on(a->bias, 4) || !words.aligned())
     return FP8_ERR_UNSUPPORTED;
   const size_t mn = size_t(a->M) * size_t(a->N);
+  // The factors come last: one of them may be the output ring's own scale_inv,
+  // which is read before the call's end writes it.
   const Span spans[] = {{a->A, size_t(a->M) * size_t(a->K), false, false, false},
                         {a->B, size_t(a->N) * size_t(a->K), false, false, false},
-                        {a->sinv_a, a->sinv_a_rows ? size_t(a->M) * 4 : 4, false, false, false},
-                        {a->sinv_b, 4, false, false, false},
                         {a->bias, size_t(a->N) * 4, false, false, false},
                         {a->aux, mn * 2, false, false, true},
                         {a->z, mn * 2, true, false, false},
-                        {a->out, mn * (out8 ? 1 : 2), true, true, false}};
-  if (!q.nothing && spans_clash(spans, 8)) return FP8_ERR_INVALID_ARG;
+                        {a->out, mn * (out8 ? 1 : 2), true, true, false},
+                        {a->sinv_a, a->sinv_a_rows ? size_t(a->M) * 4 : 4, false, false, false},
+                        {a->sinv_b, 4, false, false, false}};
+  if (!q.nothing && (spans_clash(spans, 8) || words.clash(spans, 6))) return FP8_ERR_INVALID_ARG;
+  if (overlap(a->out_amax, 4, a->sinv_a, spans[6].n) || overlap(a->out_amax, 4, a->sinv_b, 4)) return FP8_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (q.nothing) return out8 ? launch_out8_small(q, st) : FP8_OK;
   MmParams& p = q.p;

@@ -471,6 +471,8 @@ extern "C" int fp8_rmsnorm(const fp8_rmsnorm_args* p, fp8_stream_t stream) {
   if (!on(p->x, eb) || !on(p->residual, eb) || !on(p->h, eb) || !on(p->y, eb) || !on(p->gamma, p->gamma_f32 ? 4 : eb) ||
       !on(p->rstd, 4) || !on(p->row_sinv, 4))
     return FP8_ERR_UNSUPPORTED;
+  const RingWords words(ring_mode ? p->ring : fp8_ring{}, p->amax_out);
+  if (!words.aligned()) return FP8_ERR_UNSUPPORTED;
   const size_t n = size_t(p->rows) * size_t(p->cols);
   const Span spans[] = {{p->x, n * eb, false, false, true},
                         {p->residual, n * eb, false, false, true},
@@ -480,7 +482,7 @@ extern "C" int fp8_rmsnorm(const fp8_rmsnorm_args* p, fp8_stream_t stream) {
                         {p->rstd, size_t(p->rows) * 4, true, false, false},
                         {p->codes, n, true, false, false},
                         {p->row_sinv, size_t(p->rows) * 4, true, false, false}};
-  if (spans_clash(spans, 8)) return FP8_ERR_INVALID_ARG;
+  if (spans_clash(spans, 8) || words.clash(spans, 8)) return FP8_ERR_INVALID_ARG;
   if (p->rows == 0 && !ring_mode) return FP8_OK;
   NormArgs a{};
   a.x = static_cast<const uint8_t*>(p->x);

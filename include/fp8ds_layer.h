@@ -5,7 +5,8 @@
  *
  * Conventions as fp8ds.h: caller-owned device memory, asynchronous on the
  * caller's stream and the current device, negative fp8_status on an error,
- * every argument checked on the host before anything is launched.
+ * every argument checked on the host before anything is launched.  A ring's
+ * words and an amax count as outputs where overlaps are refused.
  */
 #ifndef FP8DS_LAYER_H_
 #define FP8DS_LAYER_H_
@@ -133,7 +134,8 @@ typedef enum { FP8_AUX_ADD = 0, FP8_AUX_MUL = 1 } fp8_aux_op;
  * sinv_a  one float, or (sinv_a_rows != 0) M floats: a factor per row of A, as
  *         fp8_rmsnorm's row_sinv gives them.
  * bias    float32 [N] or NULL.  aux: bf16 [M, N] or NULL.  All contiguous.
- *         out may be aux itself (a residual stream updated in place).
+ *         out may be aux itself (a residual stream updated in place); sinv_a or
+ *         sinv_b may be a word of out_ring, as it was before the call.
  * M, N >= 0, K >= 0 with K % 16 == 0; K == 0 gives z = bias; an empty output
  * still folds amax 0.  A few rows of A (16, or 32 with few columns and short
  * K) take a kernel that reads B once, straight into registers; a few hundred
@@ -189,8 +191,8 @@ int fp8_mm_act(const fp8_mm_act_args* args, fp8_stream_t stream);
  * no initial value; unused without db.  Calls that may overlap need one each.
  * rows, cols >= 0; an empty call still folds amax 0, and sets db to 0.
  * Errors: FP8_ERR_INVALID_ARG (bad enum, negative size, a missing or
- *         superfluous pointer, one ring or one amax for both outputs, a workspace
- *         that is missing or too small, an output that overlaps another argument);
+ *         superfluous pointer, rings that share a word, one amax for both outputs, a
+ *         workspace that is missing or too small, an output that overlaps another argument);
  *         FP8_ERR_UNSUPPORTED (an address not aligned to its element, a ring's
  *         scratch not 8-byte aligned, cols above 2^30, rows of 2^31 or more).
  */
