@@ -161,13 +161,32 @@ cudaError_t launch_fmt(const SkinnyArgs& a, int sms, cudaStream_t st) {
 }  // namespace
 
 // The FP8 mma of mma.sync converts its operands first, at a rate that more
-// tokens and longer rows soon reach.  Against the tile kernels, with the K split
-// where it is taken, at N x K of 1536 x 4096, 4096 x 1536, 4096 x 4096, 8192 x 4096
-// and 512 x 512 (us here / there): 8 tokens 4.7 / 5.8, 3.2 / 6.2, 5.2 / 7.8, 8.5 /
-// 13.1, 2.1 / 4.6; 16 tokens 6.5 / 5.8, 4.1 / 6.0, 6.9 / 7.8, 14.9 / 13.4, 2.5 /
-// 4.6; 24 tokens 9.4 / 6.0, 6.1 / 6.1, 10.3 / 8.1, - / 13.4, 3.3 / 4.6.
+// tokens and longer rows soon reach: a block's time grows with K and with every
+// eight tokens.  The tile kernels take the same time up to 32 tokens and, where a
+// tile's K can be split, little more for a longer one.  us here / there, by N x K:
+//                   8 tokens      16 tokens     32 tokens
+//   512 x 512       2.2 /  5.2    2.7 /  5.3    3.6 /  5.3
+//   1536 x 1536     3.0 /  5.0    3.9 /  5.1    6.1 /  5.4
+//   4096 x 1536     3.5 /  6.3    4.2 /  6.3    6.6 /  6.4
+//   1536 x 4096     4.8 /  6.0    6.6 /  6.0   10.3 /  6.0
+//   4096 x 4096     5.5 /  7.9    6.9 /  8.2   11.2 /  7.3
+//   8192 x 4096     8.6 / 13.7   15.2 / 13.9   33.2 / 12.0
+//   1536 x 8192     7.9 /  6.9   11.4 /  6.7   18.1 /  7.1
+//   1024 x 16384    9.6 /  8.5   16.9 /  8.7   32.1 /  8.9
+// Up to 16 tokens K decides; above 8, sooner with few columns, whose tiles split
+// deepest (1536 x 3328: 1.03 of the tiles' time, 2048 x 4096: 1.00), and with many,
+// by the size of the weight.  Above 16 tokens the blocks have to be resident at
+// once, three to an SM (32 tokens, 7040 x 2048: 7.0 / 8.8, 7168 x 2048: 11.7 / 8.9),
+// and K is short, but where 64-column tiles are too many for a pair of CTAs each
+// (4224 x 2048: 7.1 / 6.6, 4352 x 2048: 7.2 / 7.8).  Over 880 sizes measured (N of 256
+// to 16384, K of 256 to 16384) the kernel taken is at most 6% slower than the
+// other at all but eleven, and 16% at the worst of those (1536 x 8192, 8 tokens).
 bool skinny_wins(int64_t M, int64_t N, int64_t K, int sms) {
-  return M <= 16 || (M <= kSkinnyMaxM && K <= 1536 && (N + 15) / 16 <= 2 * int64_t(sms));
+  constexpr int64_t kPairedBlocks = 264;  // of 16 columns: 66 tiles of 64
+  const int64_t blocks = (N + 15) / 16;
+  if (M <= 8) return K <= 8192;
+  if (M <= 16) return K <= (N <= 1536 ? 3328 : 4096) && N * K < (int64_t(22) << 20);
+  return M <= kSkinnyMaxM && blocks <= 3 * int64_t(sms) && K <= (blocks > kPairedBlocks ? 2560 : 1024);
 }
 
 int launch_skinny(const SkinnyArgs& a, int sms, cudaStream_t st) {

@@ -137,8 +137,8 @@ typedef enum { FP8_AUX_ADD = 0, FP8_AUX_MUL = 1 } fp8_aux_op;
  *         out may be aux itself (a residual stream updated in place); sinv_a or
  *         sinv_b may be a word of out_ring, as it was before the call.
  * M, N >= 0, K >= 0 with K % 16 == 0; K == 0 gives z = bias; an empty output
- * still folds amax 0.  A few rows of A (16, or 32 with few columns and short
- * K) take a kernel that reads B once, straight into registers; a few hundred
+ * still folds amax 0.  A few rows of A (8, or up to 32 with short K) take a
+ * kernel that reads B once, straight into registers; a few hundred
  * rows, whose tiles leave SMs idle, share each tile's K among the CTAs of a
  * cluster.  Their sums run in other orders than the whole-tile kernel's, within
  * the same bound; the order depends on the sizes and the device only.
