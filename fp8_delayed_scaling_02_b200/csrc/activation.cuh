@@ -6,10 +6,14 @@
 //         w = 2 sqrt(2/pi) (z + 0.044715 z^3): the tanh form, since
 //         (1 + tanh(w/2)) / 2 is the logistic function of w
 //
-// act_value, for single values: p and q both come from t = e^-|w| in (0, 1]: r =
-// 1/(1+t) is one of them and t r the other, so neither cancels nor overflows.
-// The fast exponential and division are within (2 + 1.2 |w|) and 2 float32 ulp
-// (CUDA's stated bounds): far inside what the 8- and 16-bit outputs keep.
+// Everywhere from e^-w and one reciprocal, two values at a time: the tile
+// kernels' epilogue warps have some 20 issue slots per element while the next
+// tile's products run, so each operation that can is a packed one.  e^-w grows
+// without bound for w << 0: its sum's reciprocal is then 0, and so is the value.
+// One formula for every kernel, so that a row's result from one z does not depend
+// on how many rows there are.  The fast exponential (2 ulp, and |w| times the
+// rounding of its argument) and reciprocal (1 ulp) are far inside what the 8- and
+// 16-bit outputs keep.
 #pragma once
 
 #include "common.cuh"
@@ -21,29 +25,8 @@ namespace fp8ds {
 constexpr float kGeluC2 = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGeluA = 0.044715f;
 
-__device__ __forceinline__ float logistic(float w) {
-  const float t = __expf(-fabsf(w));
-  const float r = __fdividef(1.0f, 1.0f + t);
-  return w < 0.0f ? t * r : r;  // NaN: r is NaN
-}
-
 // z^2, kept finite so that 0 * z^2 stays 0 where p q has vanished.
 __device__ __forceinline__ float square_capped(float z) { return fminf(z * z, 1.0e30f); }
-
-__device__ __forceinline__ float act_value(int act, float z) {
-  switch (act) {
-    case FP8_ACT_RELU: return z < 0.0f ? 0.0f : z;  // NaN stays NaN
-    case FP8_ACT_SILU: return z * logistic(z);
-    case FP8_ACT_GELU: return z * logistic(z * fmaf(kGeluC2 * kGeluA, square_capped(z), kGeluC2));
-    default: return z;
-  }
-}
-
-// ---- two values at a time, for the product's epilogue ------------------------
-//
-// The epilogue's warps have some 20 issue slots per element while the next
-// tile's products run, so each operation that can is a packed one.  e^-w grows
-// without bound for w << 0: its sum's reciprocal is then 0, and so is the value.
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float r;
@@ -85,6 +68,18 @@ __device__ __forceinline__ void act_pair(float& a, float& b) {
     add2(x, y, 1.0f, 1.0f);
     mul2(a, b, rcp_fast(x), rcp_fast(y));
   }
+}
+
+// act of one value.
+__device__ __forceinline__ float act_one(int act, float z) {
+  float y = z, same = z;
+  switch (act) {
+    case FP8_ACT_RELU: act_pair<FP8_ACT_RELU>(y, same); break;
+    case FP8_ACT_GELU: act_pair<FP8_ACT_GELU>(y, same); break;
+    case FP8_ACT_SILU: act_pair<FP8_ACT_SILU>(y, same); break;
+    default: break;
+  }
+  return y;
 }
 
 // value and slope of a pair: q = 1 - p is off by at most 2^-24, which the slope

@@ -1747,7 +1747,7 @@ __global__ void __launch_bounds__(256) mm_act_k0_kernel(const MmParams p, int64_
   for (int64_t i = threadIdx.x; i < M * N; i += blockDim.x) {
     const float z = bias_at(p, i % N);
     if (p.z != nullptr) p.z[i] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
-    float y = act_value(p.act, z);
+    float y = act_one(p.act, z);
     if (p.aux != nullptr) {
       const float x = __uint_as_float(uint32_t(p.aux[i]) << 16);
       y = p.aux_mul ? __fmul_rn(y, x) : __fadd_rn(y, x);

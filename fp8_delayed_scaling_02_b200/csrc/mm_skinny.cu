@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kSkThreads) mm_skinny_kernel(const __grid_cons
       const float sab = __fmul_rn(p.sinv_a[p.a_rows ? m : 0], sinv_b);
       const float z = fmaf(v, sab, bias);
       if (p.z != nullptr) p.z[o] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
-      float y = act_value(p.act, z);
+      float y = act_one(p.act, z);
       if (p.aux != nullptr) {
         const float x = __uint_as_float(uint32_t(p.aux[o]) << 16);
         y = p.aux_mul ? __fmul_rn(y, x) : __fadd_rn(y, x);

@@ -141,7 +141,8 @@ typedef enum { FP8_AUX_ADD = 0, FP8_AUX_MUL = 1 } fp8_aux_op;
  * kernel that reads B once, straight into registers; a few hundred
  * rows, whose tiles leave SMs idle, share each tile's K among the CTAs of a
  * cluster.  Their sums run in other orders than the whole-tile kernel's, within
- * the same bound; the order depends on the sizes and the device only.
+ * the same bound; the order depends on the sizes and the device only.  From the
+ * sum on all of them compute the same bits.
  * Errors as fp8_mm_ex; FP8_ERR_INVALID_ARG also for an unknown act or aux_op,
  *         other layout bits, an output that overlaps another argument;
  *         FP8_ERR_UNSUPPORTED for an address not aligned to its element.
