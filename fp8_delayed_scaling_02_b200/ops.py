@@ -150,19 +150,16 @@ def _ptr(t):
 
 
 def _of_buffer(make):
-    """A read-only attribute that is made on first use and kept as long as the ring's buffer is,
-    and stays where it is.  A view made in inference mode could not be written outside it, so
-    none is made there."""
+    """A read-only attribute that is made on first use and kept as long as the ring's buffer is
+    not handed out.  A view made in inference mode could not be written outside it, so none is
+    made there."""
     name = make.__name__
 
     def get(self):
-        at = self._at()
-        made = self._made.get(name)
-        if made is not None and made[0] == at:  # else new, or buf.data = ..., buf.set_(...)
-            return made[1]
-        with torch.inference_mode(False):
-            v = make(self)
-        self._made[name] = at, v
+        v = self._made.get(name)
+        if v is None:
+            with torch.inference_mode(False):
+                v = self._made[name] = make(self)
         return v
 
     return property(get, doc=make.__doc__)
@@ -186,17 +183,17 @@ class Ring:
 
     @property
     def buf(self):
+        self._made = {}  # whoever gets the buffer may exchange its memory (buf.data = ..., buf.set_(...))
         return self._buf
 
     @buf.setter
     def buf(self, t):
         self._buf = t
-        self._at = t.data_ptr
         self._made = {}
 
     def __getstate__(self):
         state = dict(self.__dict__, buf=self._buf)
-        del state["_buf"], state["_at"], state["_made"]
+        del state["_buf"], state["_made"]
         return state
 
     def __setstate__(self, state):
@@ -205,39 +202,45 @@ class Ring:
 
     @_of_buffer
     def history(self):
-        return self.buf[0:HISTORY_LEN].view(torch.float32)
+        return self._buf[0:HISTORY_LEN].view(torch.float32)
 
     @_of_buffer
     def idx(self):
-        return self.buf[16:17]
+        return self._buf[16:17]
 
     @_of_buffer
     def scale(self):
-        return self.buf[17:18].view(torch.float32)
+        return self._buf[17:18].view(torch.float32)
 
     @_of_buffer
     def scale_inv(self):
-        return self.buf[18:19].view(torch.float32)
+        return self._buf[18:19].view(torch.float32)
 
     @_of_buffer
     def scratch(self):
-        return self.buf[20:24]
+        return self._buf[20:24]
 
-    @_of_buffer
+    @property
     def _addresses(self):
-        base = self.buf.data_ptr()
-        return base, base + 16 * 4, base + 17 * 4, base + 18 * 4, base + 20 * 4
-
-    @_of_buffer
-    def _c(self):
-        return CRing(*self._addresses)
+        """What kernels get, made anew where the memory is not what it was (a buffer handed out
+        before and exchanged since)."""
+        base = self._buf.data_ptr()
+        a = self._made.get("_addresses")
+        if a is None or a[0] != base:
+            self._made = {"_addresses": (base, base + 16 * 4, base + 17 * 4, base + 18 * 4, base + 20 * 4)}
+            a = self._made["_addresses"]
+        return a
 
     def c(self):
-        return self._c
+        a = self._addresses
+        c = self._made.get("_c")
+        if c is None:
+            c = self._made["_c"] = CRing(*a)
+        return c
 
     def state(self):
         """Host copy: (history float32[16], idx, scale, scale_inv, scratch[4])."""
-        h = self.buf.cpu()
+        h = self._buf.cpu()
         f = h.view(torch.float32)
         return f[:16].clone(), int(h[16]), float(f[17]), float(f[18]), h[20:24].clone()
 
@@ -691,21 +694,18 @@ def _on_stream(fn):
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        if args:
-            x, args = args[0], args[1:]
-        elif first in kw:
-            x = kw.pop(first)
-        else:
+        x = args[0] if args else kw.get(first)
+        if x is None:
             raise TypeError(f"{fn.__name__}() missing 1 required argument: '{first}'")
         dev = x.get_device()
         if dev < 0:
             raise ValueError("the tensors must be CUDA tensors")
         if stream is None and dev == _current_device():
-            return fn(x, *args, **kw)
+            return fn(*args, **kw)
         if stream is not None and stream.device != x.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
         with torch.cuda.device(x.device), torch.cuda.stream(stream):
-            return fn(x, *args, **kw)
+            return fn(*args, **kw)
 
     call.__signature__ = inspect.Signature([*params, inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY,
                                                                        default=None)])
@@ -731,7 +731,7 @@ def _scalar(t, dev, name):
 
 
 def _ring_on(ring, dev, name):
-    if ring.buf.get_device() != dev:
+    if ring._buf.get_device() != dev:
         raise ValueError(f"{name} is on {ring.buf.device}, expected cuda:{dev}")
 
 
@@ -808,6 +808,7 @@ def rmsnorm(x, gamma, residual=None, eps=1e-6, fmt=None, ring=None, need_rstd=Fa
         y = _empty2(rows, cols, dtype)
     rstd = _empty(rows, torch.float32) if need_rstd else None
     sinv = row_sinv = None
+    words = _NO_RING
     if fmt is None:
         if ring is not None or codes is not None or amax is not None:
             raise ValueError("codes, ring and amax need fmt")
@@ -819,14 +820,14 @@ def rmsnorm(x, gamma, residual=None, eps=1e-6, fmt=None, ring=None, need_rstd=Fa
         if ring is not None:
             _ring_on(ring, dev, "ring")
             _scalar(amax, dev, "amax")
+            words = ring._addresses
             sinv = ring.scale_inv
         elif amax is not None:
             raise ValueError("amax needs a ring")
         else:
             sinv = row_sinv = _empty(rows, torch.float32)
     args = _pack_norm(x.data_ptr(), _adr(residual), code, rows, cols, gamma.data_ptr(), f32, eps, _adr(h), _adr(y),
-                      _adr(rstd), _adr(codes), fmt or 0, *(_NO_RING if ring is None else ring._addresses), _adr(amax),
-                      _adr(row_sinv))
+                      _adr(rstd), _adr(codes), fmt or 0, *words, _adr(amax), _adr(row_sinv))
     rc = (_LIB or lib()).fp8_rmsnorm(args, _raw_stream(dev))
     if rc:
         _check(rc, "fp8_rmsnorm")

@@ -28,6 +28,19 @@ def test_views_and_addresses_follow_the_memory(how):
     assert r.state()[2] == 7.0
 
 
+def test_a_buffer_that_was_handed_out_before():
+    """The next kernel's addresses are the new ones, and the views follow them."""
+    r = ops.Ring("cpu", 2.0)
+    b = r.buf
+    for name in VIEWS:
+        getattr(r, name)
+    old, c = r._addresses, r.c()
+    b.data = ops.Ring("cpu", 5.0).buf
+    assert r._addresses[0] == b.data_ptr() != old[0]
+    assert r.c() is not c and r.c().scale == b.data_ptr() + 17 * 4
+    assert r.scale.item() == 5.0
+
+
 def test_views_are_kept_while_the_memory_stays():
     r = ops.Ring("cpu")
     assert r.scale is r.scale and r.c() is r.c()
