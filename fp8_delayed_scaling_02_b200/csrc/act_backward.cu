@@ -8,9 +8,9 @@
 //   * Without sums the tensors are one flat run of 8-element vectors, two in
 //     flight per thread, over one wave of resident blocks.
 //   * With sums a block owns a strip of 256 columns (or 64) and walks down its
-//     rows, so a thread's 8 columns stay fixed and their sums in registers; strips are cut into row chunks to
-//     fill one wave, each chunk writes one float32 row of partial sums, and a
-//     second launch adds those in order.
+//     rows, so a thread's 8 columns stay fixed and their sums in registers;
+//     strips are cut into row chunks to fill one wave, each chunk writes one
+//     float32 row of partial sums, and a second launch adds those in order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,7 +31,12 @@ namespace {
 
 constexpr int kAbThreads = 256;
 constexpr int kMaxStripCols = 256;
-// Blocks per SM of the kernels with sums, and so the registers they may use.
+// Blocks per SM of the kernels with sums, and so the registers they may use.  At
+// this count some spill (4 to 24 bytes a thread with a gate, float32 8 to 52); one
+// block fewer does not.  us here / one block fewer: gated bf16 8192 x 4096 54.3 /
+// 60.2, 8192 x 1537 58.9 / 71.9, 512 x 4096 10.5 / 9.5; without a gate bf16 8192 x
+// 4096 40.6 / 47.3, 512 x 4096 6.9 / 7.2, float32 8192 x 4096 42.8 / 43.5, 1000 x 1537
+// 9.2 / 7.9.
 constexpr int sum_blocks(bool gate) { return gate ? 3 : 4; }
 
 struct ActBwdArgs {

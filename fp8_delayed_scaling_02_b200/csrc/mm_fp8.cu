@@ -539,10 +539,14 @@ __device__ __forceinline__ void decode_tile(const MmParams& p, int t, int& b, in
 //     row per lane;
 //   * staged: z and y lie over the aux units just read, or beside them, and
 //     leave by TMA; rows that are no 16-byte multiples by guarded accesses.
-// What bounds it, 8192 x 4096 x 1536 gated, z kept, codes out, 59.7 us: the way
-// from L2 to the SMs.  The tiles' operands are 403 MB, aux, z and the codes 168
-// MB more, and each of aux and z adds what it moves (45.5 us without either,
-// 52.1 with z, 53.1 with aux), whichever unit moves it; silu adds 1 us.
+// What bounds it, 8192 x 4096 x 1536 gated, z kept, codes out, 58 to 60 us:
+// latency, no unit.  The products alone take 45.2 us, silu and codes 0.9 more, z
+// 5.6 more, aux 6.5, both 12.4; with K = 128, a twelfth of the products, silu and
+// codes take 28.5 us, with z 29.6, with aux 34.8, all 36.9 (42.7 on another GPU),
+// where their 168 MB take 25.7 at the copy rate.  So neither the products nor the
+// epilogue fills the time, and ncu shows no unit above 55% (L2 48, L1 54, tensor 46,
+// issue slots 40).  Each warp has one aux buffer and asks for the next piece only
+// when its tile is done: that chain is the first suspect.
 
 struct ActPiece {
   int i, m0, n0;  // tile ordinal of this CTA; first row and column of this warp's piece
@@ -1419,10 +1423,10 @@ __global__ void __launch_bounds__(ActCfg<BN, PAIR, EPI>::kThreads, 1)
 // through distributed shared memory, and runs the epilogue on them.  1536 x 4096
 // (N x K) with a residual, whole tiles against split ones: 64 rows 13.4 and 6.5
 // us, 128 rows 13.5 and 7.9, 256 rows 13.6 and 8.9, 512 rows 14.0 and 10.9.
-// What bounds it: the k-blocks that are left (the same rate per SM), and some
-// 5 us that no split shortens: launch, first loads, two cluster barriers, the
-// read of the other CTAs' sums (one epilogue warp per 32 rows instead of four:
-// 512 rows 15.0).
+// What is left: the k-blocks of one CTA at the pace that whole tiles have too
+// (0.35 us each; which unit sets it is not shown), and some 5 us that no split
+// shortens: launch, first loads, two cluster barriers, the read of the other CTAs'
+// flags and sums (one epilogue warp per 32 rows instead of four: 512 rows 15.0).
 template <int BN>
 struct SplitCfg {
   static constexpr int kABytes = kBM * kBK;

@@ -2,20 +2,29 @@
 // the residual's addition before it and the FP8 cast behind it, and its
 // gradient (sm_100a).
 //
-// Both are streams bound by HBM: forward 2 reads, 1 write and 1 code byte per
-// element with a residual, backward 3 reads and 1 write.  So each element is
-// read once and stays in registers, packed as it lies in memory:
+// Both are streams: forward 2 reads, 1 write and 1 code byte per element with a
+// residual, backward 3 reads and 1 write.  So each element is read once, packed as
+// it lies in memory, and stays with its thread:
 //   * a group of W warps owns a row, each thread V vectors of 8 elements at
-//     fixed columns (W = 6, V = 1 for 1536 columns: no idle lanes); the next
-//     row's loads go out before the row in work is reduced;
+//     fixed columns (1536 columns: forward W = 3, V = 2, backward W = 6, V = 1, no
+//     idle lanes); the next row's loads go out before the row in work is reduced,
+//     as far as the registers last;
 //   * the row's statistics cross lanes by shuffles and, where W > 1, warps by
 //     one shared word each and a named barrier of the group alone;
 //   * gamma comes from L1 for each row, its load ahead of the reduction: kept
-//     in registers it costs the occupancy that keeps the loads in flight;
+//     in registers it costs the occupancy that keeps the loads in flight (the
+//     forward with four vectors, which loads no row ahead, keeps it);
 //   * groups walk over the rows of one wave of resident blocks;
 //   * dgamma: partial sums per thread, then each block adds its groups' in
 //     order and writes one float32 row; a second launch adds those rows, in
 //     order, so every bit depends on the sizes, the type and the device only.
+// At 8192 x 1536 bf16 both are as near to their issue slots (64%) as to HBM: 16.4
+// us forward, 23.0 backward (13.5 and 15.4 at the copy rate).  Rows above 8192
+// columns do not fit the registers in the gradient (176 to 400 bytes of spills a
+// thread with four vectors; 2048 x 12288 float32 123 us, 61.6 at the copy rate), nor
+// in the forward of float32 (384 bytes, unaligned 996; 74.9 us, 50.0).  Rows that
+// are no multiple of 8 elements or start off the 16-byte grid pay for loads that
+// cover the neighbour's granule and stores in pieces: 8192 x 1537 39.3 and 61.3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -109,7 +118,8 @@ __device__ __forceinline__ void load_gamma8(const void* gamma, int f32, int c, i
 
 // Blocks per SM that the forward's registers allow, for the loads in flight.  Two
 // 16-bit vectors per thread, 8192 x 1536 in blocks of three, four and (126
-// registers) two: 16.6, 19.1 and 21.7 us; 8192 x 1537: 43.9, 38.9 and 56.2.
+// registers) two: 16.6, 19.1 and 21.7 us; 8192 x 1537: 43.9, 38.9 (with 48 bytes of
+// spills a thread) and 56.2.
 template <int DT, bool kAligned, int V, int NT>
 constexpr int kFwdBlocks = NT > 256 ? 1 : V == 1 ? 4 : In<DT>::kBytes == 4 ? 2 : kAligned ? 3 : 4;
 

@@ -767,7 +767,7 @@ class NormOut(NamedTuple):
     """What ``rmsnorm`` returns; what was not asked for is None."""
 
     codes: Optional[torch.Tensor]  # uint8 [rows, cols]
-    sinv: Optional[torch.Tensor]   # ring.scale_inv, or float32 [rows]
+    sinv: Optional[torch.Tensor]   # ring.scale_inv itself (the next call on the ring writes it), or float32 [rows]
     h: torch.Tensor                # the residual stream (x itself without a residual)
     rstd: Optional[torch.Tensor]   # float32 [rows]
     y: Optional[torch.Tensor]      # the norm's output in x's type
@@ -789,7 +789,9 @@ def rmsnorm(x, gamma, residual=None, eps=1e-6, fmt=None, ring=None, need_rstd=Fa
     scale per row.  fmt None returns y alone.  h, y and codes may name the
     outputs' memory; h or y may be x or residual (in place).
     Returns a NormOut; ``sinv`` goes with the codes to ``mm`` or ``mm_act``
-    (a scale per row to ``mm_act`` only).
+    (a scale per row to ``mm_act`` only).  With a ring it is ``ring.scale_inv``,
+    which the next call on that ring writes: codes kept across such a call, as
+    with two forwards before the first one's backward, need ``sinv.clone()``.
     """
     rows, cols, code = _matrix(x, "x")
     shape, dtype, dev = x.shape, x.dtype, x.get_device()

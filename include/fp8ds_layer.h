@@ -39,6 +39,9 @@ extern "C" {
  *          of the row (1 when that is 0 or not finite); row_sinv[r] = 1/scale
  *          is what fp8_mm_act takes as a row-wise sinv_a.  ring is unused.
  *          Rows on their own scales suit serving: a call keeps no state.
+ *          With a ring the codes' factor is *ring.scale_inv until the next call
+ *          on that ring writes it: where codes are kept across such a call (a
+ *          second forward before the backward), keep a copy of it with them.
  *
  * x, residual, h, y  [rows, cols] row-major, contiguous, element type dtype
  *         (fp8_in_dtype), any address aligned to the element.  h or y may be
