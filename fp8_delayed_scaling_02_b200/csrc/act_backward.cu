@@ -32,8 +32,8 @@ namespace {
 constexpr int kAbThreads = 256;
 constexpr int kMaxStripCols = 256;
 // Blocks per SM of the kernels with sums, and so the registers they may use.  At
-// this count some spill (4 to 24 bytes a thread with a gate, float32 8 to 52); one
-// block fewer does not.  us here / one block fewer: gated bf16 8192 x 4096 54.3 /
+// this count some spill (16 bits with a gate 24 bytes a thread, unaligned 48;
+// float32 16 to 56); one block fewer does not.  us here / one block fewer: gated bf16 8192 x 4096 54.3 /
 // 60.2, 8192 x 1537 58.9 / 71.9, 512 x 4096 10.5 / 9.5; without a gate bf16 8192 x
 // 4096 40.6 / 47.3, 512 x 4096 6.9 / 7.2, float32 8192 x 4096 42.8 / 43.5, 1000 x 1537
 // 9.2 / 7.9.
